@@ -1,5 +1,5 @@
 /*
- * tq.h -- C ABI of the GB300 rotated, bit-packed KV cache (turbo3 / turbo2).
+ * tq.h -- C ABI of the GB300 rotated, bit-packed KV cache (turbo4 / turbo3 / turbo2).
  *
  * The method ("llama.cpp に TurboQuant を実装", openalchemy.io): every 128-value K or V
  * block is stored as one fp16 norm plus one Lloyd-Max code per value of the block
@@ -30,6 +30,14 @@
  *                 r=j/8, k=j%8) has code bits 0,1 at bits 4k+2r, 4k+2r+1 of W_w
  *   bytes [34,50) turbo3 only: 4 u32 words V_0..V_3; value i (u=i/32, j=i%32,
  *                 p=j/8, k=j%8) has code bit 2 at bit 4k+p of V_u
+ * turbo4 (66 bytes per block) keeps codes and norms apart, in planes of the token's row:
+ *   bytes [64 b, 64 b + 64) of the row: the codes of block b, 16 little-endian u32 words;
+ *                 value i (w=i/8, k=i%8) has its magnitude index m (0..7) at bits 4k..4k+2
+ *                 of word w and its sign bit (1: negative) at bit 8k+7 for k < 4, at bit
+ *                 8(k-4)+3 for k >= 4
+ *   bytes [64 B + 2 b, 64 B + 2 b + 2) of a row of B blocks: the norm of block b, as above
+ * so that codes stay 16-byte aligned and a word of eight codes turns into eight 8-bit
+ * floating-point operands with two byte lookups.
  *
  * Cache layout (kenji.blog TinyLLaMA article, section 7: preallocate rows for the
  * maximum context, write the K/V of position N into row N, attend over rows 0..N):
@@ -62,7 +70,9 @@ extern "C" {
 
 /* Cache types: the code width in bits ("llama.cpp に TurboQuant を実装", intro and
  * "How to use": turbo3 is the default, turbo2 the experimental 2-bit type). */
-typedef enum tq_type { TQ_TURBO2 = 2, TQ_TURBO3 = 3 } tq_type;
+/* turbo4 is this library's own 4-bit type: the low five bits are the code width, bit 5 says
+ * that codes and norms lie in planes (the plain value 4 names no type). */
+typedef enum tq_type { TQ_TURBO2 = 2, TQ_TURBO3 = 3, TQ_TURBO4 = 4 | 32 } tq_type;
 
 typedef enum tq_status {
     TQ_OK = 0,
@@ -105,7 +115,7 @@ typedef struct tq_cache {
     int32_t norm_correction;
 } tq_cache;
 
-/* 50 (turbo3) or 34 (turbo2); 0 for an unknown type.  "How small does it get":
+/* 66 (turbo4), 50 (turbo3) or 34 (turbo2); 0 for an unknown type.  "How small does it get":
  * 128 values plus one FP16 norm, 0.39 / 0.27 bytes per value. */
 TQ_API size_t tq_block_bytes(int type);
 
@@ -119,12 +129,16 @@ TQ_API size_t tq_row_bytes(int type, int n_kv_heads, int head_dim);
  * does differently": after the rotation every coordinate follows the same law, so a
  * fixed, data-independent Lloyd-Max codebook is near optimal).  Centroids are solved
  * in double precision and rounded to fp32; thresholds are the fp32 midpoints.
+ * turbo4's 16 levels are the ones of least mean squared error among those that are, up to
+ * one common scale, 8-bit floating-point numbers (e4m3): +-(9, 26, 44, 64, 88, 112, 144,
+ * 192) * 2619 / 2^21, 0.83 % above the unconstrained 16-level quantiser, so that a code is an
+ * exact tensor-core operand.
  * Idempotent and cheap after the first call; must precede tq_encode / tq_decode /
  * tq_attn_decode of that type on that device.  Not thread-safe against itself. */
 TQ_API tq_status tq_codebook_init(int type, int device);
 
-/* Host copy of the type's codebook: centroids[2^type] (ascending) and
- * thresholds[2^type - 1].  Either pointer may be NULL. */
+/* Host copy of the type's codebook: centroids[2^w] (ascending) and thresholds[2^w - 1] for
+ * a code width of w bits.  Either pointer may be NULL. */
 TQ_API tq_status tq_codebook_get(int type, float *centroids, float *thresholds);
 
 /* Encode n_tokens fp16 token rows into the cache (the per-token write path,
@@ -196,6 +210,14 @@ TQ_API tq_status tq_attn_decode(const tq_cache *k, const tq_cache *v, const void
                          int64_t max_seq_len, float softmax_scale, float *out,
                          void *workspace, size_t ws_bytes, void *stream);
 
+/* tq_attn_decode with an fp16 output: out_f16 device fp16 [n_seqs][n_q_heads][head_dim],
+ * 16-byte aligned, every value rounded once (to nearest even) from the fp32 result, as the
+ * output projection of a decoder layer reads it.  Everything else as tq_attn_decode. */
+TQ_API tq_status tq_attn_decode_f16(const tq_cache *k, const tq_cache *v, const void *q_f16,
+                                    int n_seqs, int n_q_heads, const int32_t *seq_lens,
+                                    int64_t max_seq_len, float softmax_scale, void *out_f16,
+                                    void *workspace, size_t ws_bytes, void *stream);
+
 /* One decode step of a layer: append each sequence's new token to the caches, then attend
  * over the positions that include it.  This is the decode-step data flow of the kenji.blog
  * article, section 8 (the token at position N writes row N, then attends to rows 0..N),
@@ -216,6 +238,14 @@ TQ_API tq_status tq_attn_decode_append(const tq_cache *k, const tq_cache *v,
                                        const int32_t *seq_lens, int64_t max_seq_len,
                                        float softmax_scale, float *out, void *workspace,
                                        size_t ws_bytes, void *stream);
+
+/* tq_attn_decode_append with an fp16 output (see tq_attn_decode_f16). */
+TQ_API tq_status tq_attn_decode_append_f16(const tq_cache *k, const tq_cache *v,
+                                           const void *k_new_f16, const void *v_new_f16,
+                                           const void *q_f16, int n_seqs, int n_q_heads,
+                                           const int32_t *seq_lens, int64_t max_seq_len,
+                                           float softmax_scale, void *out_f16, void *workspace,
+                                           size_t ws_bytes, void *stream);
 
 /* Causal attention of a prompt chunk (multi-token / prefill) over the packed caches.
  * Query token j of the chunk sits at position pos0 + j and attends to rows 0 .. pos0 + j of
@@ -242,6 +272,11 @@ TQ_API tq_status tq_attn_decode_append(const tq_cache *k, const tq_cache *v,
 TQ_API tq_status tq_attn_prefill(const tq_cache *k, const tq_cache *v, const void *q_f16,
                                  int32_t seq_id, int64_t pos0, int64_t n_q, int n_q_heads,
                                  float softmax_scale, float *out, void *stream);
+
+/* tq_attn_prefill with an fp16 output (see tq_attn_decode_f16). */
+TQ_API tq_status tq_attn_prefill_f16(const tq_cache *k, const tq_cache *v, const void *q_f16,
+                                     int32_t seq_id, int64_t pos0, int64_t n_q, int n_q_heads,
+                                     float softmax_scale, void *out_f16, void *stream);
 
 /* Size of the fixed scratch array of tq_attn_decode_noalloc: 8 MiB per device. */
 #define TQ_NOALLOC_SCRATCH_BYTES ((size_t)8 << 20)

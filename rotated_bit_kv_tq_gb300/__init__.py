@@ -1,4 +1,4 @@
-"""GB300 rotated, bit-packed KV cache (turbo3 / turbo2) -- Python binding.
+"""GB300 rotated, bit-packed KV cache (turbo4 / turbo3 / turbo2) -- Python binding.
 
 Thin marshalling layer over the C ABI of libtq.so (include/tq.h).  PyTorch supplies
 device memory and streams; every step of encode, decode and attention runs in the
@@ -9,10 +9,10 @@ from __future__ import annotations
 
 import ctypes
 
-from ._lib import (NOALLOC_SCRATCH_BYTES, TQ_BLOCK_VALUES, TQ_TURBO2, TQ_TURBO3, TQError, TqCache,
+from ._lib import (NOALLOC_SCRATCH_BYTES, TQ_BLOCK_VALUES, TQ_TURBO2, TQ_TURBO3, TQ_TURBO4, TQError, TqCache,
                    check, load)
 
-__all__ = ["TQ_TURBO2", "TQ_TURBO3", "TQ_BLOCK_VALUES", "NOALLOC_SCRATCH_BYTES", "TQError", "TqCache", "KVCache",
+__all__ = ["TQ_TURBO2", "TQ_TURBO3", "TQ_TURBO4", "TQ_BLOCK_VALUES", "NOALLOC_SCRATCH_BYTES", "TQError", "TqCache", "KVCache",
            "block_bytes", "row_bytes", "codebook_init", "codebook_get", "encode", "encode_kv", "decode",
            "attn_workspace_bytes", "attn_decode", "attn_decode_append", "attn_prefill",
            "inject_wait_timeout", "device_status", "load"]
@@ -34,6 +34,16 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _fn(name, out):
+    """The C entry point for an output tensor: fp32, or fp16 (the _f16 entry)."""
+    import torch
+    if out is None or out.dtype == torch.float32:
+        return getattr(load(), name)
+    if out.dtype == torch.float16:
+        return getattr(load(), name + "_f16")
+    raise TQError(1, f"{name}: out must be fp32 or fp16")
+
+
 def block_bytes(tq_type: int) -> int:
     return int(load().tq_block_bytes(tq_type))
 
@@ -48,7 +58,7 @@ def codebook_init(tq_type: int, device: int = 0):
 
 def codebook_get(tq_type: int):
     import numpy as np
-    levels = 1 << tq_type
+    levels = 1 << (tq_type & 31)
     c = np.zeros(levels, np.float32)
     t = np.zeros(levels - 1, np.float32)
     check(load().tq_codebook_get(tq_type, c.ctypes.data_as(ctypes.c_void_p),
@@ -129,10 +139,10 @@ def attn_workspace_bytes(n_seqs: int, n_q_heads: int, head_dim: int, max_seq_len
 
 def attn_decode(k: KVCache, v: KVCache, q, seq_lens, max_seq_len: int, out, workspace,
                 softmax_scale: float = 0.0, stream=None):
-    """q: fp16 [n_seqs, n_q_heads, head_dim]; seq_lens int32 [n_seqs]; out fp32 like q."""
+    """q: fp16 [n_seqs, n_q_heads, head_dim]; seq_lens int32 [n_seqs]; out fp32 or fp16 like q."""
     n_seqs, n_q_heads = q.shape[0], q.shape[1]
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    check(load().tq_attn_decode(k.ref, v.ref, _ptr(q), n_seqs,
+    check(_fn("tq_attn_decode", out)(k.ref, v.ref, _ptr(q), n_seqs,
                                 n_q_heads, _ptr(seq_lens), max_seq_len, softmax_scale, _ptr(out),
                                 _ptr(workspace), ws_bytes, _stream_ptr(stream)), "tq_attn_decode")
 
@@ -143,7 +153,7 @@ def attn_decode_append(k: KVCache, v: KVCache, k_new, v_new, q, seq_lens, max_se
     seq_lens[s] - 1 of sequence s, then attention as attn_decode (seq_lens counts them)."""
     n_seqs, n_q_heads = q.shape[0], q.shape[1]
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    check(load().tq_attn_decode_append(k.ref, v.ref, _ptr(k_new),
+    check(_fn("tq_attn_decode_append", out)(k.ref, v.ref, _ptr(k_new),
                                        _ptr(v_new), _ptr(q), n_seqs, n_q_heads, _ptr(seq_lens),
                                        max_seq_len, softmax_scale, _ptr(out), _ptr(workspace),
                                        ws_bytes, _stream_ptr(stream)), "tq_attn_decode_append")
@@ -153,9 +163,9 @@ def attn_prefill(k: KVCache, v: KVCache, q, out, *, pos0: int, seq_id: int = 0,
                  softmax_scale: float = 0.0, stream=None):
     """Causal attention of a prompt chunk: q fp16 [n_q, n_q_heads, head_dim], query j at
     position pos0 + j over cache rows 0 .. pos0 + j of seq_id (its own rows encoded
-    first); out fp32 like q."""
+    first); out fp32 or fp16 like q."""
     n_q, n_q_heads = q.shape[0], q.shape[1]
-    check(load().tq_attn_prefill(k.ref, v.ref, _ptr(q), seq_id,
+    check(_fn("tq_attn_prefill", out)(k.ref, v.ref, _ptr(q), seq_id,
                                  pos0, n_q, n_q_heads, softmax_scale, _ptr(out),
                                  _stream_ptr(stream)), "tq_attn_prefill")
 

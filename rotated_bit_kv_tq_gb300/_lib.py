@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(_HERE, "libtq.so")
 
 TQ_TURBO2 = 2
 TQ_TURBO3 = 3
+TQ_TURBO4 = 4 | 32   # 4-bit codes; bit 5: codes and norms in planes of a row
 TQ_BLOCK_VALUES = 128
 # TQ_NOALLOC_SCRATCH_BYTES of tq.h: the fixed scratch of tq_attn_decode_noalloc
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -50,6 +51,10 @@ class TqCache(ctypes.Structure):
 
 _lib = None
 
+# n_seqs, n_q_heads, seq_lens, max_seq_len, scale, out, workspace, ws_bytes, stream
+_DECODE_TAIL = [ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float,
+                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+
 # name -> (restype, argtypes); the list of exported symbols the header declares
 SIGNATURES = {
     "tq_block_bytes": (ctypes.c_size_t, [ctypes.c_int]),
@@ -85,6 +90,12 @@ SIGNATURES = {
                                        ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                        ctypes.c_int64, ctypes.c_int, ctypes.c_float,
                                        ctypes.c_void_p, ctypes.c_void_p]),
+    **{name + "_f16": (ctypes.c_int, [ctypes.POINTER(TqCache)] * 2 + [ctypes.c_void_p] * lead + tail)
+       for name, lead, tail in (
+           ("tq_attn_decode", 1, _DECODE_TAIL),
+           ("tq_attn_decode_append", 3, _DECODE_TAIL),
+           ("tq_attn_prefill", 1, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                                   ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]))},
     "tq_inject_wait_timeout": (ctypes.c_int, [ctypes.c_int]),
     "tq_device_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]),
     "tq_status_str": (ctypes.c_char_p, [ctypes.c_int]),

@@ -14,15 +14,15 @@ __device__ int32_t g_status = 0;
 #if defined(TQ_TRACE_PHASES)
 __device__ unsigned long long g_phase_trace[2 * kTraceCtas][kTracePoints];
 #endif
-__constant__ Codebook c_codebook[2];
+__constant__ Codebook c_codebook[3];
 
 namespace {
 
 constexpr int kMaxDevices = 64;
-bool g_ready[kMaxDevices][2];
-Codebook g_host_cb[2];
-bool g_host_cb_done[2];
-std::atomic<float> g_h_scale[2];   // Codebook::h_scale, published once the table exists
+bool g_ready[kMaxDevices][3];
+Codebook g_host_cb[3];
+bool g_host_cb_done[3];
+std::atomic<float> g_h_scale[3];   // Codebook::h_scale, published once the table exists
 std::mutex g_mu;
 std::atomic<int> g_sm_count[kMaxDevices];
 
@@ -34,7 +34,9 @@ struct KernelState {
 std::map<std::pair<const void *, int>, KernelState> g_kernels;
 std::mutex g_kernels_mu;
 
-bool valid_type(int type) { return type == TQ_TURBO2 || type == TQ_TURBO3; }
+bool valid_type(int type) {
+    return type == TQ_TURBO2 || type == TQ_TURBO3 || type == TQ_TURBO4;
+}
 
 // Worst relative error, over the centroid magnitudes mag[0..n), of the fp16 table scaled by
 // a: |fp16(a m) / a - m| / m (evaluated in double; a is the fp32 value the kernels use).
@@ -82,13 +84,21 @@ float choose_h_scale(const float *centroid, int levels) {
 const Codebook &host_codebook(int type) {
     int i = cb_index(type);
     if (!g_host_cb_done[i]) {
-        const int levels = 1 << type;
-        double c[8];
-        solve_codebook(levels, c);
+        const int levels = 1 << code_bits(type);
+        double c[16];
+        if (type == TQ_TURBO4) {
+            for (int m = 0; m < 8; ++m) {
+                c[8 + m] = (double)kLevels4[m] * (double)kStep4;
+                c[7 - m] = -c[8 + m];
+            }
+        } else {
+            solve_codebook(levels, c);
+        }
         Codebook cb;
         std::memset(&cb, 0, sizeof cb);
         for (int j = 0; j < levels; ++j) cb.centroid[j] = (float)c[j];
-        cb.h_scale = choose_h_scale(cb.centroid, levels);
+        // turbo4: the operands are the levels' e4m3 numbers, exact in fp16 too
+        cb.h_scale = type == TQ_TURBO4 ? 1.0f / kE4m3Step4 : choose_h_scale(cb.centroid, levels);
         for (int j = 0; j < levels; ++j)
             cb.centroid_h[j] = __double2half((double)cb.h_scale * (double)cb.centroid[j]);
         // fp32 midpoints of the fp32 centroids
@@ -210,7 +220,7 @@ tq_status tq_codebook_get(int type, float *centroids, float *thresholds) {
     if (!valid_type(type)) return TQ_ERR_INVALID_ARGUMENT;
     std::lock_guard<std::mutex> lock(g_mu);
     const Codebook &cb = host_codebook(type);
-    const int levels = 1 << type;
+    const int levels = 1 << code_bits(type);
     if (centroids) std::memcpy(centroids, cb.centroid, sizeof(float) * levels);
     if (thresholds) std::memcpy(thresholds, cb.threshold, sizeof(float) * (levels - 1));
     return TQ_OK;
@@ -298,7 +308,7 @@ namespace tq {
 
 tq_status check_attn_args(const tq_cache *k, const tq_cache *v, const void *q_f16, int n_seqs,
                           int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
-                          float softmax_scale, const float *out, float *scale_out) {
+                          float softmax_scale, const void *out, float *scale_out) {
     tq_status st = validate_cache(k);
     if (st != TQ_OK) return st;
     st = validate_cache(v);
@@ -323,11 +333,11 @@ namespace {
 // tq_attn_decode and tq_attn_decode_append: the shared checks, then the workspace's.
 tq_status attn_decode_checked(const tq_cache *k, const tq_cache *v, const void *q_f16, int n_seqs,
                               int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
-                              float softmax_scale, float *out, void *workspace, size_t ws_bytes,
+                              float softmax_scale, OutPtr out, void *workspace, size_t ws_bytes,
                               void *stream, const void *k_new, const void *v_new) {
     float scale = 0.0f;
     tq_status st = check_attn_args(k, v, q_f16, n_seqs, n_q_heads, seq_lens, max_seq_len,
-                                   softmax_scale, out, &scale);
+                                   softmax_scale, out.p, &scale);
     if (st != TQ_OK) return st;
     size_t need = tq_attn_workspace_bytes(n_seqs, n_q_heads, k->head_dim, max_seq_len);
     if (need > 0 && (!workspace || ws_bytes < need)) return TQ_ERR_WORKSPACE_TOO_SMALL;
@@ -337,13 +347,11 @@ tq_status attn_decode_checked(const tq_cache *k, const tq_cache *v, const void *
 }
 }  // namespace
 
-extern "C" {
-
-tq_status tq_attn_decode_append(const tq_cache *k, const tq_cache *v, const void *k_new_f16,
-                                const void *v_new_f16, const void *q_f16, int n_seqs,
-                                int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
-                                float softmax_scale, float *out, void *workspace,
-                                size_t ws_bytes, void *stream) {
+namespace {
+tq_status append_checked(const tq_cache *k, const tq_cache *v, const void *k_new_f16,
+                         const void *v_new_f16, const void *q_f16, int n_seqs, int n_q_heads,
+                         const int32_t *seq_lens, int64_t max_seq_len, float softmax_scale,
+                         OutPtr out, void *workspace, size_t ws_bytes, void *stream) {
     if (!k_new_f16 || reinterpret_cast<uintptr_t>(k_new_f16) % 16 || !v_new_f16 ||
         reinterpret_cast<uintptr_t>(v_new_f16) % 16)
         return TQ_ERR_INVALID_ARGUMENT;
@@ -352,17 +360,9 @@ tq_status tq_attn_decode_append(const tq_cache *k, const tq_cache *v, const void
                                v_new_f16);
 }
 
-tq_status tq_attn_decode(const tq_cache *k, const tq_cache *v, const void *q_f16, int n_seqs,
-                         int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
-                         float softmax_scale, float *out, void *workspace, size_t ws_bytes,
-                         void *stream) {
-    return attn_decode_checked(k, v, q_f16, n_seqs, n_q_heads, seq_lens, max_seq_len,
-                               softmax_scale, out, workspace, ws_bytes, stream, nullptr, nullptr);
-}
-
-tq_status tq_attn_prefill(const tq_cache *k, const tq_cache *v, const void *q_f16,
+tq_status prefill_checked(const tq_cache *k, const tq_cache *v, const void *q_f16,
                           int32_t seq_id, int64_t pos0, int64_t n_q, int n_q_heads,
-                          float softmax_scale, float *out, void *stream) {
+                          float softmax_scale, OutPtr out, void *stream) {
     tq_status st = validate_cache(k);
     if (st != TQ_OK) return st;
     st = validate_cache(v);
@@ -375,12 +375,66 @@ tq_status tq_attn_prefill(const tq_cache *k, const tq_cache *v, const void *q_f1
     if (!(softmax_scale >= 0.0f) || std::isinf(softmax_scale)) return TQ_ERR_INVALID_ARGUMENT;
     if (!prefill_supported(*k, *v, n_q_heads)) return TQ_ERR_UNSUPPORTED;
     if (n_q == 0) return TQ_OK;   // empty chunk: q and out may be null
-    if (!q_f16 || !out) return TQ_ERR_INVALID_ARGUMENT;
-    if (reinterpret_cast<uintptr_t>(q_f16) % 16 || reinterpret_cast<uintptr_t>(out) % 16)
+    if (!q_f16 || !out.p) return TQ_ERR_INVALID_ARGUMENT;
+    if (reinterpret_cast<uintptr_t>(q_f16) % 16 || reinterpret_cast<uintptr_t>(out.p) % 16)
         return TQ_ERR_INVALID_ARGUMENT;
     if (softmax_scale == 0.0f) softmax_scale = 1.0f / std::sqrt((float)k->head_dim);
     return launch_prefill(*k, *v, q_f16, seq_id, pos0, n_q, n_q_heads, softmax_scale, out,
                           static_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+extern "C" {
+
+tq_status tq_attn_decode_append(const tq_cache *k, const tq_cache *v, const void *k_new_f16,
+                                const void *v_new_f16, const void *q_f16, int n_seqs,
+                                int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
+                                float softmax_scale, float *out, void *workspace,
+                                size_t ws_bytes, void *stream) {
+    return append_checked(k, v, k_new_f16, v_new_f16, q_f16, n_seqs, n_q_heads, seq_lens,
+                          max_seq_len, softmax_scale, OutPtr{out, 0}, workspace, ws_bytes, stream);
+}
+
+tq_status tq_attn_decode_append_f16(const tq_cache *k, const tq_cache *v, const void *k_new_f16,
+                                    const void *v_new_f16, const void *q_f16, int n_seqs,
+                                    int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
+                                    float softmax_scale, void *out_f16, void *workspace,
+                                    size_t ws_bytes, void *stream) {
+    return append_checked(k, v, k_new_f16, v_new_f16, q_f16, n_seqs, n_q_heads, seq_lens,
+                          max_seq_len, softmax_scale, OutPtr{out_f16, 1}, workspace, ws_bytes,
+                          stream);
+}
+
+tq_status tq_attn_decode(const tq_cache *k, const tq_cache *v, const void *q_f16, int n_seqs,
+                         int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
+                         float softmax_scale, float *out, void *workspace, size_t ws_bytes,
+                         void *stream) {
+    return attn_decode_checked(k, v, q_f16, n_seqs, n_q_heads, seq_lens, max_seq_len,
+                               softmax_scale, OutPtr{out, 0}, workspace, ws_bytes, stream,
+                               nullptr, nullptr);
+}
+
+tq_status tq_attn_decode_f16(const tq_cache *k, const tq_cache *v, const void *q_f16, int n_seqs,
+                             int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
+                             float softmax_scale, void *out_f16, void *workspace,
+                             size_t ws_bytes, void *stream) {
+    return attn_decode_checked(k, v, q_f16, n_seqs, n_q_heads, seq_lens, max_seq_len,
+                               softmax_scale, OutPtr{out_f16, 1}, workspace, ws_bytes, stream,
+                               nullptr, nullptr);
+}
+
+tq_status tq_attn_prefill(const tq_cache *k, const tq_cache *v, const void *q_f16,
+                          int32_t seq_id, int64_t pos0, int64_t n_q, int n_q_heads,
+                          float softmax_scale, float *out, void *stream) {
+    return prefill_checked(k, v, q_f16, seq_id, pos0, n_q, n_q_heads, softmax_scale,
+                           OutPtr{out, 0}, stream);
+}
+
+tq_status tq_attn_prefill_f16(const tq_cache *k, const tq_cache *v, const void *q_f16,
+                              int32_t seq_id, int64_t pos0, int64_t n_q, int n_q_heads,
+                              float softmax_scale, void *out_f16, void *stream) {
+    return prefill_checked(k, v, q_f16, seq_id, pos0, n_q, n_q_heads, softmax_scale,
+                           OutPtr{out_f16, 1}, stream);
 }
 
 tq_status tq_device_status(void *stream, int32_t *status_out) {

@@ -36,7 +36,7 @@ struct AttnParams {
     const __half *q;
     const int32_t *seq_lens;
     float *part;   // [n_seqs][n_splits][Hq][part_stride(D)]
-    float *out;    // [n_seqs][Hq][D]
+    OutPtr out;    // [n_seqs][Hq][D]
     float scale;   // softmax scale (1/sqrt(D) by default)
     int64_t max_len;
     int32_t n_q_heads, n_kv_heads, group, head_dim, nb;
@@ -93,16 +93,17 @@ __device__ __forceinline__ void warp_fwht4(float v[4], int lane) {
     }
 }
 
-// Code of value i of a packed block (layout of tq.h).
+// Code of value i of a packed block whose codes start at b (layout of tq.h).
 template <int TYPE>
 __device__ __forceinline__ int code_of(const uint8_t *b, int i) {
+    if (TYPE == TQ_TURBO4) return code4_of(b, i);
     const int j = i & 15;
     const int lb = 32 * (i >> 4) + 4 * (j & 7) + 2 * (j >> 3);
-    int code = (b[2 + (lb >> 3)] >> (lb & 7)) & 3;
+    int code = (b[lb >> 3] >> (lb & 7)) & 3;
     if (TYPE == TQ_TURBO3) {
         const int jv = i & 31;
         const int hb = 32 * (i >> 5) + 4 * (jv & 7) + (jv >> 3);
-        code |= ((b[34 + (hb >> 3)] >> (hb & 7)) & 1) << 2;
+        code |= ((b[32 + (hb >> 3)] >> (hb & 7)) & 1) << 2;
     }
     return code;
 }
@@ -135,9 +136,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_partial_kernel(const AttnPar
     float *m_run = S + Hq * TT;                                  // [Hq]
     float *l_run = m_run + Hq;                                   // [Hq]
     float *alpha = l_run + Hq;                                   // [Hq]
-    float *ck = alpha + Hq;                                      // [8]
-    float *cv = ck + 8;                                          // [8]
-    uint8_t *kt = reinterpret_cast<uint8_t *>(cv + 8);           // [TT][Rk16]
+    float *ck = alpha + Hq;                                      // [16]
+    float *cv = ck + 16;                                         // [16]
+    uint8_t *kt = reinterpret_cast<uint8_t *>(cv + 16);          // [TT][Rk16]
     kt = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(kt) + 15) & ~uintptr_t(15));
     uint8_t *vt = kt + TT * Rk16;                                // [TT][Rv16]
 
@@ -151,9 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_partial_kernel(const AttnPar
     const int64_t t_begin = (int64_t)split * p.tokens_per_split;
     const int64_t t_end = min64(len, t_begin + p.tokens_per_split);
 
-    if (tid < 8) {
-        ck[tid] = tid < (1 << TK) ? c_codebook[cb_index(TK)].centroid[tid] : 0.f;
-        cv[tid] = tid < (1 << TV) ? c_codebook[cb_index(TV)].centroid[tid] : 0.f;
+    if (tid < 16) {
+        ck[tid] = tid < (1 << code_bits(TK)) ? c_codebook[cb_index(TK)].centroid[tid] : 0.f;
+        cv[tid] = tid < (1 << code_bits(TV)) ? c_codebook[cb_index(TV)].centroid[tid] : 0.f;
     }
     for (int h = tid; h < Hq; h += kThreads) {
         m_run[h] = -INFINITY;
@@ -207,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_partial_kernel(const AttnPar
                 for (int h = 0; h < kMaxG; ++h) sc[h] = 0.f;
                 if (t < nt) {
                     for (int b = 0; b < p.nb; ++b) {
-                        const uint8_t *blk = kt + t * Rk16 + (gg * p.nb + b) * block_bytes(TK);
+                        const uint8_t *row = kt + t * Rk16;
+                        const uint8_t *blk = row + codes_offset(TK, gg * p.nb + b, Hkv * p.nb);
                         float dot[kMaxG];
 #pragma unroll
                         for (int h = 0; h < kMaxG; ++h) dot[h] = 0.f;
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_partial_kernel(const AttnPar
                             for (int h = 0; h < kMaxG; ++h)
                                 if (h < G) dot[h] = fmaf(c, qb[h * D + i], dot[h]);
                         }
-                        const float n = norm_of(blk);
+                        const float n = norm_of(row + norm_offset(TK, gg * p.nb + b, Hkv * p.nb));
 #pragma unroll
                         for (int h = 0; h < kMaxG; ++h) sc[h] = fmaf(n, dot[h], sc[h]);
                     }
@@ -271,8 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_partial_kernel(const AttnPar
 #pragma unroll
                     for (int b = 0; b < kMaxNb; ++b) {
                         if (b >= p.nb) break;
-                        const uint8_t *blk = vt + t * Rv16 + (g * p.nb + b) * block_bytes(TV);
-                        const float n = norm_of(blk);
+                        const uint8_t *row = vt + t * Rv16;
+                        const uint8_t *blk = row + codes_offset(TV, g * p.nb + b, Hkv * p.nb);
+                        const float n = norm_of(row + norm_offset(TV, g * p.nb + b, Hkv * p.nb));
                         float c[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) c[e] = cv[code_of<TV>(blk, 4 * lane + e)];
@@ -408,8 +411,8 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnParams p) {
     // inverse rotation (1/sqrt(128)) W o_b, values 4*lane .. 4*lane+3
     warp_fwht4(v, lane);
     apply_signs4(v, p.vc, 4 * lane);     // inverse D W of the V cache
-    float4 o4 = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    *reinterpret_cast<float4 *>(p.out + ((int64_t)seq * p.n_q_heads + h) * D + b * kBlock + 4 * lane) = o4;
+    store_out4(p.out, ((int64_t)seq * p.n_q_heads + h) * D + b * kBlock + 4 * lane, v[0] * inv,
+               v[1] * inv, v[2] * inv, v[3] * inv);
     if (lane == 0) TQ_PHASE(trace_slot, 3);
 }
 
@@ -467,15 +470,15 @@ __global__ void __launch_bounds__(256) attn_merge_warp_kernel(const AttnParams p
     const float inv = L > 0.f ? kInvSqrt128 / L : 0.f;
     warp_fwht4(o4, lane);                    // inverse rotation (1/sqrt(128)) W o_b
     apply_signs4(o4, p.vc, 4 * lane);        // inverse D W of the V cache
-    *reinterpret_cast<float4 *>(p.out + (seq * Hq + h) * D + b * kBlock + 4 * lane) =
-        make_float4(o4[0] * inv, o4[1] * inv, o4[2] * inv, o4[3] * inv);
+    store_out4(p.out, (seq * Hq + h) * D + b * kBlock + 4 * lane, o4[0] * inv, o4[1] * inv, o4[2] * inv,
+               o4[3] * inv);
     if (lane == 0) TQ_PHASE(trace_slot, 3);
 }
 
 size_t partial_smem(const AttnParams &p) {
     const int Rk16 = (p.kc.row_bytes + 15) & ~15, Rv16 = (p.vc.row_bytes + 15) & ~15;
     return sizeof(float) * ((size_t)p.n_q_heads * p.head_dim + (size_t)p.n_q_heads * p.tile_tokens +
-                            3 * (size_t)p.n_q_heads + 16) +
+                            3 * (size_t)p.n_q_heads + 32) +
            16 + (size_t)p.tile_tokens * (Rk16 + Rv16);
 }
 
@@ -501,6 +504,15 @@ tq_status launch_attn_t(const AttnParams &p, int n_seqs, cudaStream_t stream) {
     return launch_merge(p, n_seqs, stream);
 }
 
+template <int TK>
+tq_status launch_attn_k(int tv, const AttnParams &p, int n_seqs, cudaStream_t stream) {
+    switch (tv) {
+        case TQ_TURBO4: return launch_attn_t<TK, TQ_TURBO4>(p, n_seqs, stream);
+        case TQ_TURBO3: return launch_attn_t<TK, TQ_TURBO3>(p, n_seqs, stream);
+        default: return launch_attn_t<TK, TQ_TURBO2>(p, n_seqs, stream);
+    }
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(int n_seqs, int n_q_heads, int head_dim, int64_t max_seq_len,
@@ -514,7 +526,7 @@ size_t attn_workspace_bytes(int n_seqs, int n_q_heads, int head_dim, int64_t max
 
 tq_status launch_attn(const tq_cache &k, const tq_cache &v, const void *q, int n_seqs,
                       int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len, float scale,
-                      float *out, void *ws, size_t ws_bytes, cudaStream_t stream,
+                      OutPtr out, void *ws, size_t ws_bytes, cudaStream_t stream,
                       const void *k_new, const void *v_new) {
     AttnParams p;
     p.kc = make_view(k);
@@ -548,7 +560,7 @@ tq_status launch_attn(const tq_cache &k, const tq_cache &v, const void *q, int n
         const int cluster = grid ? 1 : n_seqs == 1 ? kClusterSplits : 1;
         tq_status st = launch_attn_mma(k, v, q, n_seqs, n_q_heads, seq_lens, max_seq_len, scale,
                                        p.part, p.n_splits, p.tokens_per_split, cluster, k_new,
-                                       v_new, grid ? out : nullptr,
+                                       v_new, grid ? out : OutPtr{nullptr, 0},
                                        grid ? static_cast<uint64_t *>(ws) : nullptr, stream);
         if (st != TQ_OK || grid) return st;
         AttnParams pm = p;
@@ -560,11 +572,11 @@ tq_status launch_attn(const tq_cache &k, const tq_cache &v, const void *q, int n
         tq_status st = launch_append(k, v, k_new, v_new, seq_lens, n_seqs, stream);
         if (st != TQ_OK) return st;
     }
-    const int tk = k.type, tv = v.type;
-    if (tk == TQ_TURBO3 && tv == TQ_TURBO3) return launch_attn_t<3, 3>(p, n_seqs, stream);
-    if (tk == TQ_TURBO2 && tv == TQ_TURBO2) return launch_attn_t<2, 2>(p, n_seqs, stream);
-    if (tk == TQ_TURBO3 && tv == TQ_TURBO2) return launch_attn_t<3, 2>(p, n_seqs, stream);
-    return launch_attn_t<2, 3>(p, n_seqs, stream);
+    switch (k.type) {
+        case TQ_TURBO4: return launch_attn_k<TQ_TURBO4>(v.type, p, n_seqs, stream);
+        case TQ_TURBO3: return launch_attn_k<TQ_TURBO3>(v.type, p, n_seqs, stream);
+        default: return launch_attn_k<TQ_TURBO2>(v.type, p, n_seqs, stream);
+    }
 }
 
 }  // namespace tq
@@ -611,6 +623,6 @@ extern "C" tq_status tq_attn_decode_noalloc(const tq_cache *k, const tq_cache *v
     if (st != TQ_OK) return st;
     // Every partial the merge reads is written by the same call first, so nothing in
     // the array needs clearing between calls.
-    return launch_attn(*k, *v, q_f16, n_seqs, n_q_heads, seq_lens, max_seq_len, scale, out,
-                       scratch, kStaticScratchBytes, static_cast<cudaStream_t>(stream));
+    return launch_attn(*k, *v, q_f16, n_seqs, n_q_heads, seq_lens, max_seq_len, scale,
+                       OutPtr{out, 0}, scratch, kStaticScratchBytes, static_cast<cudaStream_t>(stream));
 }

@@ -123,12 +123,38 @@ template <int TYPE>
 struct Quarter {
     uint32_t W0, W1, V;
 };
+// turbo4: the four 8-value words of a quarter.
+template <>
+struct Quarter<TQ_TURBO4> {
+    uint32_t w[4];
+};
+
+// The e4m3 numbers of the 8 codes of a turbo4 word: lo = values 0-3, hi = values 4-7, one per
+// byte.  Bits 0-2 of nibble k select the level of value k; the sign bits sit where a mask of
+// the word (values 0-3: bits 7, 15, 23, 31) or of the word shifted left by 4 (values 4-7) puts
+// them on the operand bytes' sign bits.
+__device__ __forceinline__ void e4m3x8(uint32_t W, uint32_t &lo, uint32_t &hi) {
+    const uint32_t sel = W & 0x77777777u;
+    lo = prmt(kE4m3Lo4, kE4m3Hi4, sel) | (W & 0x80808080u);
+    hi = prmt(kE4m3Lo4, kE4m3Hi4, sel >> 16) | ((W << 4) & 0x80808080u);
+}
+// Two e4m3 numbers (bits 0-15) as an fp16 pair; exact.
+__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t x) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(x));
+    return d;
+}
 // `row` is a 16-byte aligned packed row in shared memory; ow / ov are the word-aligned
 // byte offsets (within the row) of the quarter's low-plane and high-plane words.
 template <int TYPE>
 __device__ __forceinline__ Quarter<TYPE> load_quarter(const uint8_t *row, int ow, int ov,
                                                       uint32_t sh) {
     Quarter<TYPE> r;
+    if constexpr (TYPE == TQ_TURBO4) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(row + ow);
+        r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+        return r;
+    } else {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(row + ow);
     const uint32_t a = w[0], b = w[1], c = w[2];
     r.W0 = __funnelshift_r(a, b, sh);
@@ -140,6 +166,7 @@ __device__ __forceinline__ Quarter<TYPE> load_quarter(const uint8_t *row, int ow
         r.V = 0u;
     }
     return r;
+    }
 }
 
 // Group (ww, r) of a quarter: the 4 pairs 8ww + 4r + {0..3}.
@@ -147,7 +174,16 @@ template <int TYPE>
 __device__ __forceinline__ void group_pairs(const Quarter<TYPE> &qw, int ww, int r,
                                             const HalfTables &t, const Shifts &k,
                                             uint32_t (&o)[4]) {
+    if constexpr (TYPE == TQ_TURBO4) {
+        uint32_t lo, hi;
+        e4m3x8(qw.w[2 * ww + r], lo, hi);
+        o[0] = e4m3_to_half2(lo);
+        o[1] = e4m3_to_half2(lo >> 16);
+        o[2] = e4m3_to_half2(hi);
+        o[3] = e4m3_to_half2(hi >> 16);
+    } else {
     pairs8(t, sel8<TYPE>(ww ? qw.W1 : qw.W0, qw.V, r, 2 * ww + r, k), k.hi16, o);
+    }
 }
 
 // Rotate the query of one (head, block) pair held by a warp, four values per lane
@@ -176,7 +212,7 @@ __device__ __forceinline__ HalfTables make_tables() {
     uint32_t l[2] = {0, 0}, h[2] = {0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const uint16_t a = e < (1 << TYPE) ? __half_as_ushort(c[e]) : 0;
+        const uint16_t a = e < (1 << code_bits(TYPE)) ? __half_as_ushort(c[e]) : 0;
         l[e >> 2] |= (uint32_t)(a & 0xff) << (8 * (e & 3));
         h[e >> 2] |= (uint32_t)(a >> 8) << (8 * (e & 3));
     }

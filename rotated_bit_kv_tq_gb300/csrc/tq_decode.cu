@@ -24,7 +24,6 @@ struct DecodeParams {
 
 template <int TYPE>
 __global__ void __launch_bounds__(256) decode_kernel(const DecodeParams p) {
-    constexpr int B = block_bytes(TYPE);
     const int lane = threadIdx.x & 31;
     const int64_t blk = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (blk >= p.n_blocks) return;
@@ -36,7 +35,7 @@ __global__ void __launch_bounds__(256) decode_kernel(const DecodeParams p) {
         *out = make_float4(0.f, 0.f, 0.f, 0.f);
         return;
     }
-    const uint8_t *b = row + fb * B;
+    const uint8_t *b = row + codes_offset(TYPE, fb, p.bpr);
     const Codebook &cb = c_codebook[cb_index(TYPE)];
     // values 4*lane .. 4*lane+3
     const int i0 = 4 * lane;
@@ -46,12 +45,13 @@ __global__ void __launch_bounds__(256) decode_kernel(const DecodeParams p) {
         const int i = i0 + e;
         const int j = i & 15;
         const int lb = 32 * (i >> 4) + 4 * (j & 7) + 2 * (j >> 3);   // low-plane bit
-        int code = (b[2 + (lb >> 3)] >> (lb & 7)) & 3;
+        int code = (b[lb >> 3] >> (lb & 7)) & 3;
         if (TYPE == TQ_TURBO3) {
             const int jv = i & 31;
             const int hb = 32 * (i >> 5) + 4 * (jv & 7) + (jv >> 3);  // high-plane bit
-            code |= ((b[34 + (hb >> 3)] >> (hb & 7)) & 1) << 2;
+            code |= ((b[32 + (hb >> 3)] >> (hb & 7)) & 1) << 2;
         }
+        if (TYPE == TQ_TURBO4) code = code4_of(b, i);
         v[e] = cb.centroid[code];
     }
     // butterflies h = 1, 2 inside the lane
@@ -70,8 +70,7 @@ __global__ void __launch_bounds__(256) decode_kernel(const DecodeParams p) {
             v[e] = upper ? o - v[e] : v[e] + o;
         }
     }
-    const uint16_t nb = (uint16_t)(b[0] | (b[1] << 8));
-    const float sc = __half2float(__ushort_as_half(nb)) * kInvSqrt128;
+    const float sc = __half2float(*reinterpret_cast<const __half *>(row + norm_offset(TYPE, fb, p.bpr))) * kInvSqrt128;
     // rotation-sign variant: D W c, coordinate i negated when its sign bit is set
     float o[4];
 #pragma unroll
@@ -92,7 +91,9 @@ tq_status launch_decode(const tq_cache &src, int32_t seq_id, int64_t pos0, int64
     p.n_blocks = n_tokens * p.bpr;
     const int64_t grid = (p.n_blocks + 7) / 8;
     if (grid > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
-    if (src.type == TQ_TURBO3)
+    if (src.type == TQ_TURBO4)
+        decode_kernel<TQ_TURBO4><<<(unsigned)grid, 256, 0, stream>>>(p);
+    else if (src.type == TQ_TURBO3)
         decode_kernel<TQ_TURBO3><<<(unsigned)grid, 256, 0, stream>>>(p);
     else
         decode_kernel<TQ_TURBO2><<<(unsigned)grid, 256, 0, stream>>>(p);

@@ -91,9 +91,62 @@ __device__ __forceinline__ uint32_t collect2(uint32_t w, float v) {
     return __funnelshift_l(__float_as_uint(v), w, 2);
 }
 
+// The turbo4 codes of one block's rotated values y (fp32, rounded) and its norm, stored as
+// block fb of the packed row `out`.  The magnitude index counts the positive thresholds
+// strictly below |y|, by bisection: three comparisons with the stored y.
+__device__ __forceinline__ void encode_codes4(const float (&y)[kBlock], float n, uint16_t norm16,
+                                              uint8_t *out, int fb, int bpr, bool wide,
+                                              const CacheView &cv) {
+    const Codebook &cb = c_codebook[cb_index(TQ_TURBO4)];
+    const float *T = cb.threshold + 8;   // T[m] lies between magnitudes m and m + 1
+    uint32_t W[16];
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float v = y[8 * w + k], a = fabsf(v);
+            const bool b2 = a > T[3];
+            const bool b1 = a > (b2 ? T[5] : T[1]);
+            const bool b0 = a > (b2 ? (b1 ? T[6] : T[4]) : (b1 ? T[2] : T[0]));
+            word |= (b2 ? 4u << (4 * k) : 0u) | (b1 ? 2u << (4 * k) : 0u) | (b0 ? 1u << (4 * k) : 0u);
+            const int sb = k < 4 ? 8 * k + 7 : 8 * (k - 4) + 3;
+            word |= (__float_as_uint(v) >> 31) << sb;
+        }
+        W[w] = word;
+    }
+    uint16_t norm_out = norm16;
+    if (cv.norm_correction) {   // |x| / |c|, |c| over the same pairwise tree as the norm
+        float c2[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+            c2[i] = __fadd_rn(code_sq<TQ_TURBO4>(cb, y[i]), code_sq<TQ_TURBO4>(cb, y[i + 64]));
+#pragma unroll
+        for (int len = 64; len > 1; len >>= 1)
+#pragma unroll
+            for (int i = 0; i < len / 2; ++i) c2[i] = __fadd_rn(c2[i], c2[i + len / 2]);
+        norm_out = __half_as_ushort(__float2half_rn(fminf(__fdiv_rn(n, __fsqrt_rn(c2[0])), 65504.0f)));
+    }
+    uint8_t *codes = out + codes_offset(TQ_TURBO4, fb, bpr);
+    *reinterpret_cast<uint16_t *>(out + norm_offset(TQ_TURBO4, fb, bpr)) = norm_out;
+    if (wide) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            reinterpret_cast<uint4 *>(codes)[c] = make_uint4(W[4 * c], W[4 * c + 1], W[4 * c + 2], W[4 * c + 3]);
+    } else {
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            reinterpret_cast<uint16_t *>(codes)[2 * w] = (uint16_t)(W[w] & 0xffffu);
+            reinterpret_cast<uint16_t *>(codes)[2 * w + 1] = (uint16_t)(W[w] >> 16);
+        }
+    }
+}
+
+// Encode the staged fp16 block f of a tile into block fb of the packed row `out` (2-byte
+// aligned in shared memory; 16-byte when `wide`).
 template <int TYPE>
-__device__ __forceinline__ void encode_one(const uint8_t *blk_in, int f, uint8_t *out,
-                                           const CacheView &cv) {
+__device__ __forceinline__ void encode_one(const uint8_t *blk_in, int f, uint8_t *out, int fb,
+                                           int bpr, bool wide, const CacheView &cv) {
     const Codebook &cb = c_codebook[cb_index(TYPE)];
     // ---- 1. load and convert once
     float x[kBlock];
@@ -174,6 +227,10 @@ __device__ __forceinline__ void encode_one(const uint8_t *blk_in, int f, uint8_t
         x[i] = y2.x;
         x[i + 1] = y2.y;
     }
+    if constexpr (TYPE == TQ_TURBO4) {
+        encode_codes4(x, n, norm16, out, fb, bpr, wide, cv);
+        return;
+    }
     uint32_t W[8], SP[8];
     const float t_lo = TYPE == TQ_TURBO3 ? cb.threshold[4] : cb.threshold[2];
     const float t_mid = TYPE == TQ_TURBO3 ? cb.threshold[5] : 0.0f;
@@ -230,7 +287,7 @@ __device__ __forceinline__ void encode_one(const uint8_t *blk_in, int f, uint8_t
         norm_out = __half_as_ushort(__float2half_rn(fminf(r, 65504.0f)));
     }
     // ---- 6. stage the packed block (2-byte aligned in shared memory)
-    uint16_t *o = reinterpret_cast<uint16_t *>(out);
+    uint16_t *o = reinterpret_cast<uint16_t *>(out + fb * block_bytes(TYPE));
     o[0] = norm_out;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
@@ -253,7 +310,6 @@ __global__ void __launch_bounds__(kThreads, 3) encode_kernel(const EncodeParams 
     const EncodeParams &p = blockIdx.y ? p1 : p0;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     EncodeSmem<TYPE> &sm = *reinterpret_cast<EncodeSmem<TYPE> *>(smem_raw);
-    constexpr int B = block_bytes(TYPE);
     pdl_wait();
     pdl_launch_dependents();
 
@@ -290,7 +346,11 @@ __global__ void __launch_bounds__(kThreads, 3) encode_kernel(const EncodeParams 
 
         const int nblk = rows * p.bpr;
         const int f = threadIdx.x;
-        if (f < nblk) encode_one<TYPE>(sm.in[it & 1] + f * 256, f, sm.out + f * B, p.dst);
+        if (f < nblk) {
+            const int r = (int)fast_div((uint32_t)f, p.bpr_magic);
+            encode_one<TYPE>(sm.in[it & 1] + f * 256, f, sm.out + r * p.row_bytes, f - r * p.bpr,
+                             p.bpr, (p.row_bytes & 15) == 0, p.dst);
+        }
         __syncthreads();
 
         // ---- write whole rows out
@@ -354,7 +414,6 @@ __global__ void __launch_bounds__(32 * kWarpPathWarps) encode_warp_kernel(const 
     pdl_wait();
     pdl_launch_dependents();
     const EncodeParams &p = blockIdx.y ? p1 : p0;
-    constexpr int B = block_bytes(TYPE);
     const int lane = threadIdx.x & 31;
     const int64_t gw = (int64_t)blockIdx.x * kWarpPathWarps + (threadIdx.x >> 5);
     if (gw >= p.n_tokens * p.bpr) return;   // whole warp
@@ -368,7 +427,7 @@ __global__ void __launch_bounds__(32 * kWarpPathWarps) encode_warp_kernel(const 
     if (lane == 0) row = row_ptr(p.dst, seq, pos);   // records an out-of-range row once
     row = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(row), 0));
     if (!row) return;
-    warp_store_block<TYPE>(row + (int64_t)jb * B, wb, lane);
+    warp_store_block<TYPE>(row, jb, p.bpr, wb, lane);
 }
 
 template <int TYPE>
@@ -387,6 +446,24 @@ tq_status launch_encode_any(const EncodeParams &p0, const EncodeParams &p1, int 
     const int64_t blocks = max64(p0.n_tokens * p0.bpr, p1.n_tokens * p1.bpr);
     return blocks <= kWarpPathMaxBlocks ? launch_encode_warp_t<TYPE>(p0, p1, n_caches, stream)
                                         : launch_encode_t<TYPE>(p0, p1, n_caches, stream);
+}
+
+tq_status launch_encode_typed(int type, const EncodeParams &p0, const EncodeParams &p1, int n_caches,
+                              cudaStream_t stream) {
+    switch (type) {
+        case TQ_TURBO4: return launch_encode_any<TQ_TURBO4>(p0, p1, n_caches, stream);
+        case TQ_TURBO3: return launch_encode_any<TQ_TURBO3>(p0, p1, n_caches, stream);
+        default: return launch_encode_any<TQ_TURBO2>(p0, p1, n_caches, stream);
+    }
+}
+
+tq_status launch_warp_typed(int type, const EncodeParams &p0, const EncodeParams &p1, int n_caches,
+                            cudaStream_t stream) {
+    switch (type) {
+        case TQ_TURBO4: return launch_encode_warp_t<TQ_TURBO4>(p0, p1, n_caches, stream);
+        case TQ_TURBO3: return launch_encode_warp_t<TQ_TURBO3>(p0, p1, n_caches, stream);
+        default: return launch_encode_warp_t<TQ_TURBO2>(p0, p1, n_caches, stream);
+    }
 }
 
 EncodeParams make_params(const tq_cache &dst, const void *src, int64_t n_tokens, int64_t stride,
@@ -419,8 +496,7 @@ tq_status launch_encode(const tq_cache &dst, const void *src, int64_t n_tokens, 
                         const int32_t *seq_ids, const int32_t *positions, int32_t seq_id,
                         int64_t pos0, cudaStream_t stream) {
     const EncodeParams p = make_params(dst, src, n_tokens, stride, seq_ids, positions, seq_id, pos0);
-    return dst.type == TQ_TURBO3 ? launch_encode_any<TQ_TURBO3>(p, p, 1, stream)
-                                 : launch_encode_any<TQ_TURBO2>(p, p, 1, stream);
+    return launch_encode_typed(dst.type, p, p, 1, stream);
 }
 
 tq_status launch_encode_kv(const tq_cache &k, const tq_cache &v, const void *k_src,
@@ -435,8 +511,7 @@ tq_status launch_encode_kv(const tq_cache &k, const tq_cache &v, const void *k_s
         if (st != TQ_OK) return st;
         return launch_encode(v, v_src, n_tokens, v_stride, seq_ids, positions, seq_id, pos0, stream);
     }
-    return k.type == TQ_TURBO3 ? launch_encode_any<TQ_TURBO3>(pk, pv, 2, stream)
-                               : launch_encode_any<TQ_TURBO2>(pk, pv, 2, stream);
+    return launch_encode_typed(k.type, pk, pv, 2, stream);
 }
 
 // Decode-step append for shapes the fused attention kernel does not take: sequence s's new
@@ -450,14 +525,11 @@ tq_status launch_append(const tq_cache &k, const tq_cache &v, const void *k_new,
     pk.lens = seq_lens;
     pv.lens = seq_lens;
     if (k.type != v.type) {
-        tq_status st = k.type == TQ_TURBO3 ? launch_encode_warp_t<TQ_TURBO3>(pk, pk, 1, stream)
-                                           : launch_encode_warp_t<TQ_TURBO2>(pk, pk, 1, stream);
+        tq_status st = launch_warp_typed(k.type, pk, pk, 1, stream);
         if (st != TQ_OK) return st;
-        return v.type == TQ_TURBO3 ? launch_encode_warp_t<TQ_TURBO3>(pv, pv, 1, stream)
-                                   : launch_encode_warp_t<TQ_TURBO2>(pv, pv, 1, stream);
+        return launch_warp_typed(v.type, pv, pv, 1, stream);
     }
-    return k.type == TQ_TURBO3 ? launch_encode_warp_t<TQ_TURBO3>(pk, pv, 2, stream)
-                               : launch_encode_warp_t<TQ_TURBO2>(pk, pv, 2, stream);
+    return launch_warp_typed(k.type, pk, pv, 2, stream);
 }
 
 }  // namespace tq

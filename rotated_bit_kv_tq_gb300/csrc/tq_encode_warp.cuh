@@ -20,17 +20,18 @@ namespace {
 // m = #{positive thresholds below |y|} (the codebook is symmetric).
 template <int TYPE>
 __device__ __forceinline__ float code_sq(const Codebook &cb, float y) {
-    constexpr int L = 1 << TYPE;
+    constexpr int L = 1 << code_bits(TYPE);
     const float a = fabsf(y);
-    int m = a > cb.threshold[L / 2] ? 1 : 0;
-    if (TYPE == TQ_TURBO3) m += (a > cb.threshold[5] ? 1 : 0) + (a > cb.threshold[6] ? 1 : 0);
+    int m = 0;
+#pragma unroll
+    for (int j = L / 2; j <= L - 2; ++j) m += a > cb.threshold[j] ? 1 : 0;
     const float c = cb.centroid[L / 2 + m];
     return __fmul_rn(c, c);
 }
 
 // The packed form of one block, spread over the warp: the norm (every lane), this lane's
 // 16-value low-plane word (complete in lanes 4j) and 32-value high-plane word (complete in
-// lanes 8j, turbo3 only).
+// lanes 8j, turbo3 only); turbo4: this lane's 8-value word (complete in lanes 2j).
 struct WarpBlock {
     uint16_t norm16;
     uint32_t wlo, whi;
@@ -47,7 +48,7 @@ __device__ __forceinline__ uint2 warp_block_load(const __half *src, int lane) {
 template <int TYPE>
 __device__ __forceinline__ WarpBlock warp_encode_raw(uint2 raw, const CacheView &cv, int lane) {
     const Codebook &cb = c_codebook[cb_index(TYPE)];
-    constexpr int L = 1 << TYPE;
+    constexpr int L = 1 << code_bits(TYPE);
     const float2 f01 = __half22float2(*reinterpret_cast<const __half2 *>(&raw.x));
     const float2 f23 = __half22float2(*reinterpret_cast<const __half2 *>(&raw.y));
     float x[4] = {f01.x, f01.y, f23.x, f23.y};
@@ -108,6 +109,11 @@ __device__ __forceinline__ WarpBlock warp_encode_raw(uint2 raw, const CacheView 
         uint32_t m = 0;
 #pragma unroll
         for (int j = L / 2; j <= L - 2; ++j) m += a > cb.threshold[j] ? 1u : 0u;
+        if (TYPE == TQ_TURBO4) {   // magnitude in nibble 4 (lane & 1) + e, sign apart
+            const uint32_t s = signbit(y) ? 1u : 0u;
+            wlo |= (m << (16 * (lane & 1) + 4 * e)) | (s << (8 * e + ((lane & 1) ? 3 : 7)));
+            continue;
+        }
         const uint32_t c = signbit(y) ? (uint32_t)(L / 2 - 1) - m : (uint32_t)(L / 2) + m;
         const int jl = 4 * (lane & 3) + e;          // value index within its 16-value word
         wlo |= (c & 3u) << (4 * (jl & 7) + 2 * (jl >> 3));
@@ -117,7 +123,7 @@ __device__ __forceinline__ WarpBlock warp_encode_raw(uint2 raw, const CacheView 
         }
     }
     wlo |= __shfl_xor_sync(0xffffffffu, wlo, 1);
-    wlo |= __shfl_xor_sync(0xffffffffu, wlo, 2);
+    if (TYPE != TQ_TURBO4) wlo |= __shfl_xor_sync(0xffffffffu, wlo, 2);
     if (TYPE == TQ_TURBO3) {
         whi |= __shfl_xor_sync(0xffffffffu, whi, 1);
         whi |= __shfl_xor_sync(0xffffffffu, whi, 2);
@@ -133,10 +139,19 @@ __device__ __forceinline__ WarpBlock warp_encode_block(const __half *src, const 
     return warp_encode_raw<TYPE>(warp_block_load(src, lane), cv, lane);
 }
 
-// Store a warp-encoded block at `o` (2-byte aligned; the block's byte layout of tq.h).
+// Store a warp-encoded block as block fb of the packed row at `row` (bpr blocks, 2-byte
+// aligned; the byte layout of tq.h).
 template <int TYPE>
-__device__ __forceinline__ void warp_store_block(uint8_t *dst, const WarpBlock &wb, int lane) {
-    uint16_t *o = reinterpret_cast<uint16_t *>(dst);
+__device__ __forceinline__ void warp_store_block(uint8_t *row, int fb, int bpr, const WarpBlock &wb,
+                                                 int lane) {
+    if (TYPE == TQ_TURBO4) {
+        uint16_t *c = reinterpret_cast<uint16_t *>(row + codes_offset(TYPE, fb, bpr));
+        if (lane == 0) *reinterpret_cast<uint16_t *>(row + norm_offset(TYPE, fb, bpr)) = wb.norm16;
+        // lanes 2w and 2w + 1 both hold word w: each stores one half
+        c[lane] = (uint16_t)(lane & 1 ? wb.wlo >> 16 : wb.wlo & 0xffffu);
+        return;
+    }
+    uint16_t *o = reinterpret_cast<uint16_t *>(row + fb * block_bytes(TYPE));
     if (lane == 0) o[0] = wb.norm16;
     if ((lane & 3) == 0) {
         o[1 + 2 * (lane >> 2)] = (uint16_t)(wb.wlo & 0xffffu);

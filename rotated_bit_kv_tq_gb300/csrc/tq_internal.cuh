@@ -16,7 +16,20 @@ constexpr int kBlock = TQ_BLOCK_VALUES;  // values per block
 // The binary32 value nearest to 1/sqrt(128) = 2^-3.5.
 constexpr float kInvSqrt128 = 0x1.6a09e6p-4f;
 
-__host__ __device__ constexpr int block_bytes(int type) { return 2 + kBlock * type / 8; }
+// Code width in bits of a cache type (TQ_TURBO4 carries its layout flag above bit 4).
+__host__ __device__ constexpr int code_bits(int type) { return type & 31; }
+__host__ __device__ constexpr int block_bytes(int type) { return 2 + kBlock * code_bits(type) / 8; }
+
+// Where block fb of a row of bpr blocks keeps its codes and its norm (byte offsets in the
+// row).  turbo2 / turbo3 rows hold whole blocks, norm first; turbo4 rows hold the codes of
+// all blocks, then the norms ("Packed block layout" in tq.h).
+constexpr int kCodeBytes4 = kBlock / 2;
+__host__ __device__ constexpr int codes_offset(int type, int fb, int bpr) {
+    return type == TQ_TURBO4 ? fb * kCodeBytes4 : fb * block_bytes(type) + 2;
+}
+__host__ __device__ constexpr int norm_offset(int type, int fb, int bpr) {
+    return type == TQ_TURBO4 ? bpr * kCodeBytes4 + 2 * fb : fb * block_bytes(type);
+}
 
 // Split-K CTAs of one cluster for a single sequence: the tensor-core attention kernel merges
 // the partials of these consecutive splits in distributed shared memory before writing one
@@ -107,6 +120,17 @@ __device__ __forceinline__ uint8_t *row_ptr(const CacheView &c, int64_t seq, int
     return c.base + row * (int64_t)c.row_bytes;
 }
 
+// Ascending centroid index (0 .. 15) of value i of a turbo4 block whose codes start at c:
+// magnitude m at bits 4k .. 4k + 2 of its 8-value word, the sign bit at bit 8k + 7 (k < 4)
+// or 8 (k - 4) + 3.
+__device__ __forceinline__ int code4_of(const uint8_t *c, int i) {
+    const int k = i & 7;
+    const uint8_t *w = c + 4 * (i >> 3);
+    const int m = (w[k >> 1] >> (4 * (k & 1))) & 7;
+    const int sb = k < 4 ? 8 * k + 7 : 8 * (k - 4) + 3;
+    return ((w[sb >> 3] >> (sb & 7)) & 1) ? 7 - m : 8 + m;
+}
+
 // Programmatic dependent launch.  Kernels launched with the programmatic-serialization
 // attribute may start while the previous kernel in the stream is still running; they call
 // pdl_wait() before their first global-memory access (it returns once that kernel has
@@ -168,23 +192,62 @@ struct PdlConfig {
 #endif  // __CUDACC__
 
 // ------------------------------------------------------------------ codebook tables
-// Uploaded by tq_codebook_init.  Index 0 = turbo2 (4 levels), 1 = turbo3 (8 levels).
+// Uploaded by tq_codebook_init.  Index 0 = turbo2 (4 levels), 1 = turbo3 (8 levels),
+// 2 = turbo4 (16 levels).
 struct Codebook {
-    float centroid[8];
-    float threshold[7];
+    float centroid[16];
+    float threshold[15];
     // fp16 operands of the tensor-core attention kernels: centroid_h[j] = fp16(h_scale *
     // centroid[j]), with h_scale in [1, 2) chosen so that every scaled centroid lies within
     // a few 1e-5 (relative) of an fp16 value.  The kernels divide h_scale out in fp32 (the
     // query scale on the key side, the value norms on the value side), so a centroid's
     // systematic fp16 error drops from up to 2.3e-4 to 2.2e-5 (turbo3) and 7e-7 (turbo2).
-    __half centroid_h[8];
+    __half centroid_h[16];
     float h_scale;
 };
+
+// turbo4: the 16 levels are +-kLevels4[m] * kStep4, and every kLevels4[m] / 16 is an 8-bit
+// floating-point number (e4m3, bytes kE4m3Levels4), so that a code becomes an exact
+// tensor-core operand with one byte lookup per four codes.  The levels are the ones of least
+// mean squared error among all sets of 16 such numbers with a common scale, for one
+// coordinate of a uniformly random unit vector in R^128: found by dynamic programming over
+// the e4m3 grid for each scale, they lie 0.83 % above the unconstrained 16-level Lloyd-Max
+// quantiser (normalised MSE 0.009392 against 0.009314).  kStep4 has 12 significant bits
+// (2619 / 2^21), so that the fp32 centroids and midpoints are exact products.
+constexpr int kLevels4[8] = {9, 26, 44, 64, 88, 112, 144, 192};
+constexpr float kStep4 = 2619.0f / 2097152.0f;
+constexpr uint32_t kE4m3Lo4 = 0x48433D31u, kE4m3Hi4 = 0x54514E4Bu;   // levels 0-3, 4-7, over 16
+constexpr float kE4m3Step4 = 16.0f * kStep4;   // a level = its e4m3 number times this
+
 #if defined(__CUDACC__)
-extern __constant__ Codebook c_codebook[2];
+extern __constant__ Codebook c_codebook[3];
 #endif
 
-__host__ __device__ constexpr int cb_index(int type) { return type == TQ_TURBO3 ? 1 : 0; }
+__host__ __device__ constexpr int cb_index(int type) {
+    return type == TQ_TURBO4 ? 2 : type == TQ_TURBO3 ? 1 : 0;
+}
+
+// An attention output: fp32 or fp16 (each value rounded once, to nearest even, when stored).
+struct OutPtr {
+    void *p;
+    int32_t f16;
+};
+#if defined(__CUDACC__)
+__device__ __forceinline__ void store_out(const OutPtr &o, int64_t i, float v) {
+    if (o.f16) static_cast<__half *>(o.p)[i] = __float2half_rn(v);
+    else static_cast<float *>(o.p)[i] = v;
+}
+// Four consecutive values from index i (a multiple of 4).
+__device__ __forceinline__ void store_out4(const OutPtr &o, int64_t i, float a, float b, float c, float d) {
+    if (o.f16) {
+        const __half2 lo = __floats2half2_rn(a, b), hi = __floats2half2_rn(c, d);
+        *reinterpret_cast<uint2 *>(static_cast<__half *>(o.p) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(o.p) + i) = make_float4(a, b, c, d);
+    }
+}
+#endif
 
 // ------------------------------------------------------------------ host side
 bool codebook_ready(int type, int device);
@@ -202,7 +265,7 @@ tq_status validate_cache(const tq_cache *c);
 // success *scale_out is the softmax scale to use (1/sqrt(head_dim) when 0 is passed).
 tq_status check_attn_args(const tq_cache *k, const tq_cache *v, const void *q_f16, int n_seqs,
                           int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len,
-                          float softmax_scale, const float *out, float *scale_out);
+                          float softmax_scale, const void *out, float *scale_out);
 
 // Kernel launchers (one per .cu file).
 tq_status launch_encode(const tq_cache &dst, const void *src, int64_t n_tokens, int64_t stride,
@@ -220,7 +283,7 @@ size_t attn_workspace_bytes(int n_seqs, int n_q_heads, int head_dim, int64_t max
 // seq_lens[s] - 1 before attending (the tensor-core kernel does it in the same launch).
 tq_status launch_attn(const tq_cache &k, const tq_cache &v, const void *q, int n_seqs,
                       int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len, float scale,
-                      float *out, void *ws, size_t ws_bytes, cudaStream_t stream,
+                      OutPtr out, void *ws, size_t ws_bytes, cudaStream_t stream,
                       const void *k_new = nullptr, const void *v_new = nullptr);
 tq_status launch_append(const tq_cache &k, const tq_cache &v, const void *k_new, const void *v_new,
                         const int32_t *seq_lens, int n_seqs, cudaStream_t stream);
@@ -236,8 +299,11 @@ bool grid_merge_fits(int n_seqs, int n_splits);
 tq_status launch_attn_mma(const tq_cache &k, const tq_cache &v, const void *q, int n_seqs,
                           int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len, float scale,
                           float *part, int n_splits, int tokens_per_split, int cluster,
-                          const void *k_new, const void *v_new, float *out, uint64_t *bar,
+                          const void *k_new, const void *v_new, OutPtr out, uint64_t *bar,
                           cudaStream_t stream);
+
+// The same kernel's turbo4 pairs (tq_attn_mma_t4.cu); params is that kernel's parameter block.
+tq_status launch_attn_mma_t4(int tk, int tv, int nb, const void *params, int n_seqs, cudaStream_t stream);
 
 // Fault injection of tq_inject_wait_timeout (tq_attn_mma.cu).
 tq_status inject_wait_timeout(int n_calls);
@@ -245,7 +311,7 @@ tq_status inject_wait_timeout(int n_calls);
 // Prompt-chunk attention on the 5th-generation tensor cores (tq_prefill_tc.cu).
 bool prefill_supported(const tq_cache &k, const tq_cache &v, int n_q_heads);
 tq_status launch_prefill(const tq_cache &k, const tq_cache &v, const void *q, int32_t seq_id,
-                         int64_t pos0, int64_t n_q, int n_q_heads, float scale, float *out,
+                         int64_t pos0, int64_t n_q, int n_q_heads, float scale, OutPtr out,
                          cudaStream_t stream);
 
 // h_scale of a type's fp16 centroid table (see Codebook); 1 for an unknown type.

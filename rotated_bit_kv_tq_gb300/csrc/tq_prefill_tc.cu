@@ -56,6 +56,7 @@ constexpr uint32_t kTcPollLimit = 1u << 24;   // polls without progress of the M
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256, kTmemP = 384;
 constexpr float kTcLog2e = 1.4426950408889634f;
+constexpr float kVDown4 = 0.015625f;   // turbo4 V norms in the fp16 tile: |v| c <= 12288
 
 // mbarriers
 // Buffer b of a double-buffered resource serves tiles b, b + 2, ...; a waiter for tile i
@@ -77,7 +78,7 @@ enum {
 struct TcParams {
     CacheView kc, vc;
     const __half *q;        // [n_q][Hq][128] fp16
-    float *out;             // [n_q][Hq][128] fp32
+    OutPtr out;             // [n_q][Hq][head_dim]
     int64_t pos0, n_q;
     int32_t seq, n_q_heads, group, bq;
     int32_t n_kv_heads;
@@ -283,13 +284,29 @@ __device__ __forceinline__ uint32_t win_chunk(int key, int c) {
 // Producer thread pt of a group stages key pt of tile [t0, t0 + keys) of its cache: the
 // 16-byte chunks covering head g's block with cp.async when rows are 16-byte multiples (so
 // the chunks are aligned and lie inside the row), else the block's 2-byte halves with plain
-// loads.
+// loads.  Returns a turbo4 block's norm bits, whose load need not have landed (the caller
+// holds the register until it decodes the tile); the other types stage the norm with the codes.
 template <int TYPE>
-__device__ __forceinline__ void tc_stage(const CacheView &cv, int32_t seq, bool chunked,
+__device__ __forceinline__ uint32_t tc_stage(const CacheView &cv, int32_t seq, bool chunked,
                                          uint8_t *raw, uint8_t *ok, int g, int64_t t0,
                                          int64_t n_keys, int pt) {
     const int64_t t = t0 + pt;
     const uint8_t *row = t < n_keys ? row_ptr(cv, seq, t) : nullptr;
+    if (TYPE == TQ_TURBO4) {   // 64 bytes of codes (window bytes 0-63) and the norm apart
+        if (row) {
+            if (chunked) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    cp_async16(smem_u32(raw + win_chunk(pt, c)), row + kCodeBytes4 * g + 16 * c);
+            } else {
+                const uint16_t *src = reinterpret_cast<const uint16_t *>(row + kCodeBytes4 * g);
+                for (int h = 0; h < kCodeBytes4 / 2; ++h)
+                    *reinterpret_cast<uint16_t *>(raw + win_chunk(pt, h >> 3) + 2 * (h & 7)) = src[h];
+            }
+        }
+        ok[pt] = row ? 1 : 0;
+        return row ? *reinterpret_cast<const uint16_t *>(row + norm_offset(TYPE, g, cv.row_bytes / block_bytes(TYPE))) : 0;
+    }
     constexpr int bb = block_bytes(TYPE);
     const int bo = g * bb, x0 = bo & ~15, lead = bo & 15;
     if (row) {
@@ -306,7 +323,12 @@ __device__ __forceinline__ void tc_stage(const CacheView &cv, int32_t seq, bool 
         }
     }
     ok[pt] = row ? 1 : 0;
+    return 0;
 }
+
+// Registers that hold a staged block: 13 words (turbo2 / turbo3), 16 of codes and the norm
+// (turbo4).
+__host__ __device__ constexpr int win_words(int type) { return type == TQ_TURBO4 ? 17 : 13; }
 
 // Producer thread pt reads key pt's staged window and brings its block to byte 0:
 // n[j] = block bytes 4j .. 4j + 3.  The block's offset in the window, lead (its offset in the
@@ -315,7 +337,19 @@ __device__ __forceinline__ void tc_stage(const CacheView &cv, int32_t seq, bool 
 // select levels, then a funnel shift by the remaining 0 or 2 bytes.  The staging area is
 // free again once this returns.
 template <int TYPE>
-__device__ __forceinline__ void tc_window(const uint8_t *raw, int g, int pt, uint32_t (&n)[13]) {
+__device__ __forceinline__ void tc_window(const uint8_t *raw, uint32_t nrm, int g, int pt,
+                                          uint32_t (&n)[win_words(TYPE)]) {
+    if constexpr (TYPE == TQ_TURBO4) {   // n[0..15] the codes, n[16] the norm
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(raw + win_chunk(pt, c));
+            n[4 * c] = u.x;
+            n[4 * c + 1] = u.y;
+            n[4 * c + 2] = u.z;
+            n[4 * c + 3] = u.w;
+        }
+        n[16] = nrm;
+    } else {
     constexpr int B = block_bytes(TYPE);
     uint32_t w[17];
 #pragma unroll
@@ -336,6 +370,7 @@ __device__ __forceinline__ void tc_window(const uint8_t *raw, int g, int pt, uin
     for (int j = 0; j < 14; ++j) w[j] = s2 ? w[j + 2] : w[j];
 #pragma unroll
     for (int j = 0; j < 13; ++j) n[j] = __funnelshift_r(w[j], w[j + 1], sh);
+    }
 }
 
 // Producer thread pt decodes key pt from its block bytes n (tc_window): K into fp16
@@ -344,25 +379,34 @@ __device__ __forceinline__ void tc_window(const uint8_t *raw, int g, int pt, uin
 // NC, c_off (MN only): the tile holds NC coordinates and this block fills coordinates
 // c_off .. c_off + 127 (8-key groups NC * 16 bytes apart).
 template <int TYPE, bool MN, int NC = 128>
-__device__ __forceinline__ void tc_decode(const uint32_t (&n)[13], bool present,
+__device__ __forceinline__ void tc_decode(const uint32_t (&n)[win_words(TYPE)], bool present,
                                           const HalfTables &tab, uint8_t *tile, float *norm,
                                           int pt, int c_off = 0) {
     const Shifts shifts = {2u, 4u, 1u << 16, 1u << 30, 1u << 31};
     // the norm: block bytes 0-1, 0 for an absent row.  V folds it into the tile values
     // (|v| c); K keeps it apart (norm[]) and the scores are scaled in fp32, which keeps one
     // fp16 rounding on the score path
-    const __half nrm = present ? __ushort_as_half((uint16_t)(n[0] & 0xffffu)) : __ushort_as_half(0);
-    const __half2 n2 = __halves2half2(nrm, nrm);
+    // turbo4's operands reach 12, so its V norms are taken down by kVDown4 (an exact scaling
+    // of all but subnormal results), which the output scale undoes
+    constexpr int kNormWord = TYPE == TQ_TURBO4 ? 16 : 0;
+    const __half nrm = present ? __ushort_as_half((uint16_t)(n[kNormWord] & 0xffffu)) : __ushort_as_half(0);
+    const __half nsc = TYPE == TQ_TURBO4 && MN ? __hmul(nrm, __float2half_rn(kVDown4)) : nrm;
+    const __half2 n2 = __halves2half2(nsc, nsc);
     if (!MN) norm[pt] = __half2float(nrm);
 #pragma unroll
     for (int q4 = 0; q4 < 4; ++q4) {
         // the quarter's low-plane bytes are block bytes 2 + 8 q4 .., its high-plane word
         // block bytes 34 + 4 q4 ..
         Quarter<TYPE> qw;
+        if constexpr (TYPE == TQ_TURBO4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qw.w[e] = n[4 * q4 + e];
+        } else {
         qw.W0 = __funnelshift_r(n[2 * q4], n[2 * q4 + 1], 16);
         qw.W1 = __funnelshift_r(n[2 * q4 + 1], n[2 * q4 + 2], 16);
         if (TYPE == TQ_TURBO3) qw.V = __funnelshift_r(n[8 + q4], n[9 + q4], 16);
         else qw.V = 0u;
+        }
 #pragma unroll
         for (int ww = 0; ww < 2; ++ww)
 #pragma unroll
@@ -412,15 +456,16 @@ __device__ __forceinline__ void tc_produce(const TcParams &p, TcSmem &sm, int g,
     uint8_t *ok = sm.ok[IS_V ? 1 : 0];
     const HalfTables tab = make_tables<TYPE>();
     const int free_bar = IS_V ? kBarPvFree : kBarSFree, full_bar = IS_V ? kBarVFull : kBarKFull;
-    if (n_tiles > 0) tc_stage<TYPE>(cv, p.seq, chunked, raw, ok, g, (int64_t)tile0 * kTcKeys, n_keys, pt);
+    uint32_t nrm = 0;   // the staged tile's norm (turbo4)
+    if (n_tiles > 0) nrm = tc_stage<TYPE>(cv, p.seq, chunked, raw, ok, g, (int64_t)tile0 * kTcKeys, n_keys, pt);
     cp_async_commit();
     for (int i = 0; i < n_tiles; ++i) {
         const int b = i & 1;
         cp_async_wait<0>();   // this thread's bytes of tile i have landed
-        uint32_t nb[13];
-        tc_window<TYPE>(raw, g, pt, nb);
+        uint32_t nb[win_words(TYPE)];
+        tc_window<TYPE>(raw, nrm, g, pt, nb);
         const bool present = ok[pt] != 0;
-        if (i + 1 < n_tiles) tc_stage<TYPE>(cv, p.seq, chunked, raw, ok, g, (int64_t)(tile0 + i + 1) * kTcKeys, n_keys, pt);
+        if (i + 1 < n_tiles) nrm = tc_stage<TYPE>(cv, p.seq, chunked, raw, ok, g, (int64_t)(tile0 + i + 1) * kTcKeys, n_keys, pt);
         cp_async_commit();
         if (i >= 2 && !*abort_v &&
             !tc_wait(smem_u32(&sm.bar[free_bar + b]), (uint32_t)(((i - 2) >> 1) & 1)))
@@ -697,14 +742,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const TcParam
         }
         if (write) {
             const float inv = l_row > 0.f ? p.out_scale / l_row : 0.f;
-            float4 *dst = reinterpret_cast<float4 *>(p.out + ((j0 + jl) * Hq + g * G + hl) * (int64_t)kBlock + 64 * h);
+            const int64_t dst = ((j0 + jl) * Hq + g * G + hl) * (int64_t)kBlock + 64 * h;
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
                 float v4[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     v4[e] = __uint_as_float(__float_as_uint(o[4 * c + e] * inv) ^ sign_mask(p.vc, 64 * h + 4 * c + e));
-                dst[c] = make_float4(v4[0], v4[1], v4[2], v4[3]);
+                store_out4(p.out, dst + 4 * c, v4[0], v4[1], v4[2], v4[3]);
             }
         }
     } else if (warp < kTcMmaWarp) {
@@ -1066,15 +1111,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
                 for (int e = 0; e < 4; ++e) o[4 * c + e] = h ? pv[e] - o[4 * c + e] : o[4 * c + e] + pv[e];
             }
             if (valid && done) {
-                float4 *dst = reinterpret_cast<float4 *>(p.out + ((j0 + jl) * Hq + g * G + hl) * (int64_t)D +
-                                                         kBlock * blk + 64 * h);
+                const int64_t dst = ((j0 + jl) * Hq + g * G + hl) * (int64_t)D + kBlock * blk + 64 * h;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     float v4[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         v4[e] = __uint_as_float(__float_as_uint(o[4 * c + e] * inv) ^ sign_mask(p.vc, 64 * h + 4 * c + e));
-                    dst[c] = make_float4(v4[0], v4[1], v4[2], v4[3]);
+                    store_out4(p.out, dst + 4 * c, v4[0], v4[1], v4[2], v4[3]);
                 }
             }
         }
@@ -1086,17 +1130,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
         if (tid - kTcSoftmax < kTcGroup) {
             // K: double-buffered tiles, one 16 KB tile per block
             const HalfTables tab = make_tables<TK>();
+            uint32_t nrm = 0;
             if (n_tiles > 0)
-                tc_stage<TK>(p.kc, p.seq, p.chunked_k, sm.raw_k[blk], sm.ok[blk], 2 * g + blk, 0, n_keys, key);
+                nrm = tc_stage<TK>(p.kc, p.seq, p.chunked_k, sm.raw_k[blk], sm.ok[blk], 2 * g + blk, 0, n_keys, key);
             cp_async_commit();
             for (int i = 0; i < n_tiles; ++i) {
                 const int b = i & 1;
                 cp_async_wait<0>();
-                uint32_t nb[13];
-                tc_window<TK>(sm.raw_k[blk], 2 * g + blk, key, nb);
+                uint32_t nb[win_words(TK)];
+                tc_window<TK>(sm.raw_k[blk], nrm, 2 * g + blk, key, nb);
                 const bool present = sm.ok[blk][key] != 0;
                 if (i + 1 < n_tiles)
-                    tc_stage<TK>(p.kc, p.seq, p.chunked_k, sm.raw_k[blk], sm.ok[blk], 2 * g + blk,
+                    nrm = tc_stage<TK>(p.kc, p.seq, p.chunked_k, sm.raw_k[blk], sm.ok[blk], 2 * g + blk,
                                  (int64_t)(i + 1) * k2Keys, n_keys, key);
                 cp_async_commit();
                 if (i >= 2 && !*abort_v && !tc_wait(bar(k2BarKFree + b), (uint32_t)(((i - 2) >> 1) & 1)))
@@ -1109,16 +1154,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
         } else {
             // V: one 256-coordinate tile, rewritten once the previous tile's P V is done
             const HalfTables tab = make_tables<TV>();
+            uint32_t nrm = 0;
             if (n_tiles > 0)
-                tc_stage<TV>(p.vc, p.seq, p.chunked_v, sm.raw_v[blk], sm.ok[2 + blk], 2 * g + blk, 0, n_keys, key);
+                nrm = tc_stage<TV>(p.vc, p.seq, p.chunked_v, sm.raw_v[blk], sm.ok[2 + blk], 2 * g + blk, 0, n_keys, key);
             cp_async_commit();
             for (int i = 0; i < n_tiles; ++i) {
                 cp_async_wait<0>();
-                uint32_t nb[13];
-                tc_window<TV>(sm.raw_v[blk], 2 * g + blk, key, nb);
+                uint32_t nb[win_words(TV)];
+                tc_window<TV>(sm.raw_v[blk], nrm, 2 * g + blk, key, nb);
                 const bool present = sm.ok[2 + blk][key] != 0;
                 if (i + 1 < n_tiles)
-                    tc_stage<TV>(p.vc, p.seq, p.chunked_v, sm.raw_v[blk], sm.ok[2 + blk], 2 * g + blk,
+                    nrm = tc_stage<TV>(p.vc, p.seq, p.chunked_v, sm.raw_v[blk], sm.ok[2 + blk], 2 * g + blk,
                                  (int64_t)(i + 1) * k2Keys, n_keys, key);
                 cp_async_commit();
                 if (i >= 1 && !*abort_v &&
@@ -1221,6 +1267,24 @@ tq_status launch_tc_t(const TcParams &p, unsigned n_ctas, cudaStream_t stream) {
     return check_cuda(cudaLaunchKernelEx(&lc.cfg, prefill_tc_kernel<TK, TV>, p));
 }
 
+template <int TK>
+tq_status launch_tc256_k(int tv, const TcParams &p, unsigned n_ctas, cudaStream_t stream) {
+    switch (tv) {
+        case TQ_TURBO4: return launch_tc256_t<TK, TQ_TURBO4>(p, n_ctas, stream);
+        case TQ_TURBO3: return launch_tc256_t<TK, TQ_TURBO3>(p, n_ctas, stream);
+        default: return launch_tc256_t<TK, TQ_TURBO2>(p, n_ctas, stream);
+    }
+}
+
+template <int TK>
+tq_status launch_tc_k(int tv, const TcParams &p, unsigned n_ctas, cudaStream_t stream) {
+    switch (tv) {
+        case TQ_TURBO4: return launch_tc_t<TK, TQ_TURBO4>(p, n_ctas, stream);
+        case TQ_TURBO3: return launch_tc_t<TK, TQ_TURBO3>(p, n_ctas, stream);
+        default: return launch_tc_t<TK, TQ_TURBO2>(p, n_ctas, stream);
+    }
+}
+
 }  // namespace
 
 bool prefill_supported(const tq_cache &k, const tq_cache &v, int n_q_heads) {
@@ -1229,7 +1293,7 @@ bool prefill_supported(const tq_cache &k, const tq_cache &v, int n_q_heads) {
 }
 
 tq_status launch_prefill(const tq_cache &k, const tq_cache &v, const void *q, int32_t seq_id,
-                         int64_t pos0, int64_t n_q, int n_q_heads, float scale, float *out,
+                         int64_t pos0, int64_t n_q, int n_q_heads, float scale, OutPtr out,
                          cudaStream_t stream) {
     if (!prefill_supported(k, v, n_q_heads)) return TQ_ERR_UNSUPPORTED;
     if (n_q == 0) return TQ_OK;
@@ -1249,7 +1313,7 @@ tq_status launch_prefill(const tq_cache &k, const tq_cache &v, const void *q, in
     // the fp16 centroid tables are scaled by h_scale (Codebook); the query scale divides the
     // K table's out, the output scale the V table's
     p.score_scale = scale * kTcLog2e * kInvSqrt128 / centroid_h_scale(k.type);
-    p.out_scale = kInvSqrt128 / centroid_h_scale(v.type);
+    p.out_scale = kInvSqrt128 / centroid_h_scale(v.type) / (v.type == TQ_TURBO4 ? kVDown4 : 1.0f);
     p.n_kv_heads = k.n_kv_heads;
     p.n_qblocks = (n_q + p.bq - 1) / p.bq;
     const int64_t n_ctas = p.n_qblocks * k.n_kv_heads;
@@ -1257,10 +1321,11 @@ tq_status launch_prefill(const tq_cache &k, const tq_cache &v, const void *q, in
     const unsigned nc = (unsigned)n_ctas;
     if (k.head_dim == 2 * kBlock) {   // one CTA per query block, no key split
         p.split = 1;
-        if (k.type == TQ_TURBO3 && v.type == TQ_TURBO3) return launch_tc256_t<3, 3>(p, nc, stream);
-        if (k.type == TQ_TURBO2 && v.type == TQ_TURBO2) return launch_tc256_t<2, 2>(p, nc, stream);
-        if (k.type == TQ_TURBO3 && v.type == TQ_TURBO2) return launch_tc256_t<3, 2>(p, nc, stream);
-        return launch_tc256_t<2, 3>(p, nc, stream);
+        switch (k.type) {
+            case TQ_TURBO4: return launch_tc256_k<TQ_TURBO4>(v.type, p, nc, stream);
+            case TQ_TURBO3: return launch_tc256_k<TQ_TURBO3>(v.type, p, nc, stream);
+            default: return launch_tc256_k<TQ_TURBO2>(v.type, p, nc, stream);
+        }
     }
     // Split each query block's key tiles over a cluster of two CTAs when that fills the last
     // wave of one-CTA-per-SM launches markedly better (the two CTAs both rotate the queries,
@@ -1274,10 +1339,11 @@ tq_status launch_prefill(const tq_cache &k, const tq_cache &v, const void *q, in
         const int64_t max_tiles = (pos0 + n_q + kTcKeys - 1) / kTcKeys;
         p.split = (max_tiles >= 4 && e2 > 1.08 * e1) ? 2 : 1;
     }
-    if (k.type == TQ_TURBO3 && v.type == TQ_TURBO3) return launch_tc_t<3, 3>(p, nc, stream);
-    if (k.type == TQ_TURBO2 && v.type == TQ_TURBO2) return launch_tc_t<2, 2>(p, nc, stream);
-    if (k.type == TQ_TURBO3 && v.type == TQ_TURBO2) return launch_tc_t<3, 2>(p, nc, stream);
-    return launch_tc_t<2, 3>(p, nc, stream);
+    switch (k.type) {
+        case TQ_TURBO4: return launch_tc_k<TQ_TURBO4>(v.type, p, nc, stream);
+        case TQ_TURBO3: return launch_tc_k<TQ_TURBO3>(v.type, p, nc, stream);
+        default: return launch_tc_k<TQ_TURBO2>(v.type, p, nc, stream);
+    }
 }
 
 }  // namespace tq
