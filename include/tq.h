@@ -307,6 +307,76 @@ TQ_API tq_status tq_attn_decode_noalloc(const tq_cache *k, const tq_cache *v,
                                         const int32_t *seq_lens, int64_t max_seq_len,
                                         float softmax_scale, float *out, void *stream);
 
+/* ------------------------------------------------------------------ pages of paged caches
+ * The K and V caches of all layers of a model share one page table, so one set of page
+ * numbers, one table and one list of reference counts serve them all.  Plain data; the caller
+ * allocates the three device arrays (zero refcounts, zero seq_lens, -1 in page_table: an empty
+ * pool) and passes page_table and seq_lens on to the caches and the attention calls.
+ *   Sequence s holds the pages page_table[s][0 .. ceil(seq_lens[s] / page_tokens)); the
+ *   entries behind them are -1.  refcounts[p] says how many sequences hold page p (0: free).
+ *   A page that a sequence's last row shares with free rows belongs to that sequence alone
+ *   (fork copies it), so appending never writes into a shared page. */
+typedef struct tq_page_pool {
+    int32_t n_pages;            /* >= 1 */
+    int32_t page_tokens;        /* rows per page, a multiple of 32 */
+    int32_t n_seqs;             /* rows of page_table; fewer than 2^31 entries in all */
+    int32_t max_pages_per_seq;  /* columns; max_pages_per_seq * page_tokens < 2^31 */
+    int32_t *page_table;        /* device int32 [n_seqs][max_pages_per_seq] */
+    int32_t *seq_lens;          /* device int32 [n_seqs]: rows held (attention's seq_lens) */
+    int32_t *refcounts;         /* device int32 [n_pages] */
+} tq_page_pool;
+
+/* Caches one page call takes: the K and V caches of 128 layers. */
+#define TQ_PAGES_MAX_CACHES 256
+
+/* Shared by the calls below.  Lists are device int32 arrays; `workspace` is device scratch of
+ * at least tq_pages_workspace_bytes(n_pages, n_seqs, n) bytes (n: the list's length, 0 for
+ * compact; n_seqs 0 for copy), 16-byte aligned, that needs no initialisation and keeps nothing
+ * between calls; calls that share one must be ordered.  Results do not depend on timing: free
+ * pages are taken lowest number first, in list order.  What only the GPU can see (a sequence
+ * or page number out of range, a length beyond the table, a sequence listed twice, a pool
+ * without enough free pages) skips that list entry, leaves its sequence as it was and records
+ * TQ_ERR_OUT_OF_RANGE for tq_device_status.  All caches must be paged, with the pool's
+ * page_tokens and at least its n_pages; at most TQ_PAGES_MAX_CACHES of them (else
+ * TQ_ERR_UNSUPPORTED).  n == 0 is a no-op. */
+TQ_API size_t tq_pages_workspace_bytes(int32_t n_pages, int32_t n_seqs, int32_t n_items);
+
+/* Make room for n_new[i] more rows of sequence seqs[i]: the pages they need are taken from the
+ * free ones and seq_lens grows by n_new[i] (the new rows are then written by tq_encode_kv or
+ * tq_attn_decode_append).  An entry that needs pages is skipped when the free ones do not
+ * suffice for entries 0 .. i together. */
+TQ_API tq_status tq_pages_extend(const tq_page_pool *pool, const int32_t *seqs, const int32_t *n_new,
+                                 int32_t n, void *workspace, size_t ws_bytes, void *stream);
+
+/* Make sequence children[i], which must be empty, a copy of parents[i]: whole pages are shared
+ * (their counts grow), the last, partly filled page is copied into a free page in every cache
+ * (its filled rows only).  A parent may be listed several times; an empty parent makes an
+ * empty child.  Rows of other pages are not touched. */
+TQ_API tq_status tq_pages_fork(const tq_page_pool *pool, const tq_cache *const *caches,
+                               int32_t n_caches, const int32_t *parents, const int32_t *children,
+                               int32_t n, void *workspace, size_t ws_bytes, void *stream);
+
+/* Empty the listed sequences: their pages' counts fall by one, their table entries become -1,
+ * their lengths 0.  A sequence listed twice, or already empty, is freed once. */
+TQ_API tq_status tq_pages_free(const tq_page_pool *pool, const int32_t *seqs, int32_t n, void *stream);
+
+/* Move the pages in use to the lowest page numbers, 0 .. U - 1: the used pages numbered U and
+ * up go, in order, to the free pages below U in every cache, and `out` receives the renumbered
+ * table, the counts and the lengths.  `out` has the pool's sizes; its arrays are the pool's own
+ * (in place) or all others (then the old table stays valid for attention calls already issued
+ * with it, as the moved pages' old rows are not overwritten).  *n_used (device int32, or null)
+ * receives U. */
+TQ_API tq_status tq_pages_compact(const tq_page_pool *pool, const tq_page_pool *out,
+                                  const tq_cache *const *caches, int32_t n_caches, int32_t *n_used,
+                                  void *workspace, size_t ws_bytes, void *stream);
+
+/* Copy the first rows[i] rows (rows null: all) of page src[i] to page dst[i] in every cache.  A
+ * pair whose destination is also a source, or an earlier pair's destination, is skipped and
+ * recorded, so the order of the copies does not matter. */
+TQ_API tq_status tq_pages_copy(const tq_cache *const *caches, int32_t n_caches, const int32_t *src,
+                               const int32_t *dst, const int32_t *rows, int32_t n, void *workspace,
+                               size_t ws_bytes, void *stream);
+
 /* Fault injection for tests of the bounded device-side waits: failure detection without a
  * GPU fault (nothing traps, hangs or touches bad memory).  The next
  * n_calls launches of the tensor-core decode-attention kernel (tq_attn_decode,

@@ -10,12 +10,13 @@ from __future__ import annotations
 import ctypes
 
 from ._lib import (NOALLOC_SCRATCH_BYTES, TQ_BLOCK_VALUES, TQ_TURBO2, TQ_TURBO3, TQ_TURBO4, TQError, TqCache,
-                   check, load)
+                   TqPagePool, check, load)
 
 __all__ = ["TQ_TURBO2", "TQ_TURBO3", "TQ_TURBO4", "TQ_BLOCK_VALUES", "NOALLOC_SCRATCH_BYTES", "TQError", "TqCache", "KVCache",
            "block_bytes", "row_bytes", "codebook_init", "codebook_get", "encode", "encode_kv", "decode",
            "attn_workspace_bytes", "attn_decode", "attn_decode_append", "attn_prefill",
-           "inject_wait_timeout", "device_status", "load"]
+           "PagePool", "CacheGroup", "pages_extend", "pages_fork", "pages_free", "pages_compact", "pages_copy",
+           "pages_workspace_bytes",           "inject_wait_timeout", "device_status", "load"]
 
 
 # Pointers and stream handles are passed as plain integers (the argtypes are c_void_p), which
@@ -168,6 +169,109 @@ def attn_prefill(k: KVCache, v: KVCache, q, out, *, pos0: int, seq_id: int = 0,
     check(_fn("tq_attn_prefill", out)(k.ref, v.ref, _ptr(q), seq_id,
                                  pos0, n_q, n_q_heads, softmax_scale, _ptr(out),
                                  _stream_ptr(stream)), "tq_attn_prefill")
+
+
+class CacheGroup:
+    """The caches one page call works on (the K and V caches of all layers), as the C calls
+    take them; make it once and pass it to every call."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        self.n = len(self.caches)
+        self.array = (ctypes.POINTER(TqCache) * self.n)(*[ctypes.pointer(c.view) for c in self.caches])
+
+
+def _group(caches):
+    return caches if isinstance(caches, CacheGroup) else CacheGroup(caches)
+
+
+class PagePool:
+    """Pages of paged caches: an int32 device ``page_table`` [n_seqs, max_pages_per_seq] (-1: no
+    page), ``seq_lens`` [n_seqs] and ``refcounts`` [n_pages].  Arrays that are not passed are
+    made, as an empty pool.  Give ``page_table`` to the KVCache objects and ``seq_lens`` to the
+    attention calls.  The pool keeps one workspace: order its calls (one stream, or events)."""
+
+    def __init__(self, n_pages: int, page_tokens: int, n_seqs: int, max_pages_per_seq: int, *,
+                 device=None, page_table=None, seq_lens=None, refcounts=None):
+        import torch
+        device = device if device is not None else "cuda"
+        shapes = ((n_seqs, max_pages_per_seq), (n_seqs,), (n_pages,))
+        fill = (-1, 0, 0)
+        made = []
+        for t, shape, f in zip((page_table, seq_lens, refcounts), shapes, fill):
+            if t is None:
+                t = torch.full(shape, f, dtype=torch.int32, device=device)
+            if tuple(t.shape) != shape or t.dtype != torch.int32 or not t.is_contiguous():
+                raise TQError(1, f"PagePool: a contiguous int32 tensor of shape {shape} is wanted")
+            made.append(t)
+        self.page_table, self.seq_lens, self.refcounts = made
+        self.n_pages, self.n_seqs = n_pages, n_seqs
+        self.view = TqPagePool(n_pages, page_tokens, n_seqs, max_pages_per_seq, *[t.data_ptr() for t in made])
+        self.ref = ctypes.byref(self.view)
+        self._ws = torch.empty(max(16, self._ws_bytes(n_seqs)), dtype=torch.uint8, device=device)
+
+    def _ws_bytes(self, n_items: int) -> int:
+        return int(load().tq_pages_workspace_bytes(self.n_pages, self.n_seqs, n_items))
+
+    def workspace(self, n_items: int):
+        """Scratch for a list of n_items entries (made for n_seqs entries, grown when a longer
+        list comes)."""
+        if n_items > self.n_seqs:
+            import torch
+            need = self._ws_bytes(n_items)
+            if need > self._ws.numel():
+                self._ws = torch.empty(need, dtype=torch.uint8, device=self._ws.device)
+        return self._ws
+
+
+def _list(t, n=None):
+    """A device list of the page calls: contiguous int32, of length n where given."""
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise TQError(1, "page call: a contiguous int32 list is wanted")
+    return t.data_ptr()
+
+
+def pages_extend(pool: PagePool, seqs, n_new, stream=None):
+    """Room for n_new[i] more rows of sequence seqs[i] (int32 device lists)."""
+    n = seqs.shape[0]
+    ws = pool.workspace(n)
+    check(load().tq_pages_extend(pool.ref, _list(seqs), _list(n_new, n), n, ws.data_ptr(), ws.numel(),
+                                 _stream_ptr(stream)), "tq_pages_extend")
+
+
+def pages_fork(pool: PagePool, caches, parents, children, stream=None):
+    """The empty sequences children[i] become copies of parents[i]; caches: a CacheGroup or a
+    list of every KVCache on the pool's pages."""
+    g, n = _group(caches), parents.shape[0]
+    ws = pool.workspace(n)
+    check(load().tq_pages_fork(pool.ref, g.array, g.n, _list(parents), _list(children, n), n,
+                               ws.data_ptr(), ws.numel(), _stream_ptr(stream)), "tq_pages_fork")
+
+
+def pages_free(pool: PagePool, seqs, stream=None):
+    """Empty the listed sequences (int32 device list)."""
+    check(load().tq_pages_free(pool.ref, _list(seqs), seqs.shape[0], _stream_ptr(stream)), "tq_pages_free")
+
+
+def pages_compact(pool: PagePool, caches, out: PagePool | None = None, n_used=None, stream=None):
+    """Move the pages in use to the lowest numbers; the renumbered pool goes to ``out`` (the
+    pool itself by default), the count of used pages to ``n_used`` (int32 device tensor)."""
+    g, ws = _group(caches), pool.workspace(0)
+    check(load().tq_pages_compact(pool.ref, (out or pool).ref, g.array, g.n, _ptr(n_used), ws.data_ptr(),
+                                  ws.numel(), _stream_ptr(stream)), "tq_pages_compact")
+
+
+def pages_copy(caches, src, dst, rows=None, *, workspace, stream=None):
+    """Copy the first rows[i] rows (all by default) of page src[i] to page dst[i] in every cache;
+    workspace: uint8 device tensor of pages_workspace_bytes(n_pages, 0, len(src)) bytes."""
+    g, n = _group(caches), src.shape[0]
+    check(load().tq_pages_copy(g.array, g.n, _list(src), _list(dst, n), _list(rows, n) if rows is not None else None,
+                               n, _ptr(workspace), workspace.numel(), _stream_ptr(stream)), "tq_pages_copy")
+
+
+def pages_workspace_bytes(n_pages: int, n_seqs: int, n_items: int) -> int:
+    return int(load().tq_pages_workspace_bytes(n_pages, n_seqs, n_items))
 
 
 def inject_wait_timeout(n_calls: int):

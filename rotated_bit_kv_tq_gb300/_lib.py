@@ -49,7 +49,24 @@ class TqCache(ctypes.Structure):
     ]
 
 
+class TqPagePool(ctypes.Structure):
+    """Mirror of struct tq_page_pool."""
+    _fields_ = [
+        ("n_pages", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("n_seqs", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("refcounts", ctypes.c_void_p),
+    ]
+
+
 _lib = None
+
+_POOL = ctypes.POINTER(TqPagePool)
+_CACHES = [ctypes.POINTER(ctypes.POINTER(TqCache)), ctypes.c_int32]
+_WS = [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]   # workspace, ws_bytes, stream
 
 # n_seqs, n_q_heads, seq_lens, max_seq_len, scale, out, workspace, ws_bytes, stream
 _DECODE_TAIL = [ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float,
@@ -96,6 +113,12 @@ SIGNATURES = {
            ("tq_attn_decode_append", 3, _DECODE_TAIL),
            ("tq_attn_prefill", 1, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                    ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]))},
+    "tq_pages_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
+    "tq_pages_extend": (ctypes.c_int, [_POOL, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32] + _WS),
+    "tq_pages_fork": (ctypes.c_int, [_POOL] + _CACHES + [ctypes.c_void_p] * 2 + [ctypes.c_int32] + _WS),
+    "tq_pages_free": (ctypes.c_int, [_POOL, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "tq_pages_compact": (ctypes.c_int, [_POOL, _POOL] + _CACHES + [ctypes.c_void_p] + _WS),
+    "tq_pages_copy": (ctypes.c_int, _CACHES + [ctypes.c_void_p] * 3 + [ctypes.c_int32] + _WS),
     "tq_inject_wait_timeout": (ctypes.c_int, [ctypes.c_int]),
     "tq_device_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]),
     "tq_status_str": (ctypes.c_char_p, [ctypes.c_int]),
