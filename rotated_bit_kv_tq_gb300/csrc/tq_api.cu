@@ -299,7 +299,11 @@ tq_status tq_decode(const tq_cache *src, int32_t seq_id, int64_t pos0, int64_t n
 size_t tq_attn_workspace_bytes(int n_seqs, int n_q_heads, int head_dim, int64_t max_seq_len) {
     if (n_seqs < 1 || n_q_heads < 1 || head_dim < kBlock || head_dim % kBlock || max_seq_len < 0)
         return 0;
-    return attn_workspace_bytes(n_seqs, n_q_heads, head_dim, max_seq_len, device_sm_count());
+    // the caches' types are not known here: enough for either kind of kernel
+    const int sms = device_sm_count();
+    const size_t a = attn_workspace_bytes(n_seqs, n_q_heads, head_dim, max_seq_len, sms);
+    const size_t b = attn_t4_workspace_bytes(n_seqs, n_q_heads, head_dim, sms);
+    return b > a ? b : a;
 }
 
 }  // extern "C"
@@ -339,7 +343,7 @@ tq_status attn_decode_checked(const tq_cache *k, const tq_cache *v, const void *
     tq_status st = check_attn_args(k, v, q_f16, n_seqs, n_q_heads, seq_lens, max_seq_len,
                                    softmax_scale, out.p, &scale);
     if (st != TQ_OK) return st;
-    size_t need = tq_attn_workspace_bytes(n_seqs, n_q_heads, k->head_dim, max_seq_len);
+    const size_t need = attn_need_bytes(*k, *v, n_seqs, n_q_heads, max_seq_len);
     if (need > 0 && (!workspace || ws_bytes < need)) return TQ_ERR_WORKSPACE_TOO_SMALL;
     if (workspace && reinterpret_cast<uintptr_t>(workspace) % 16) return TQ_ERR_INVALID_ARGUMENT;
     return launch_attn(*k, *v, q_f16, n_seqs, n_q_heads, seq_lens, max_seq_len, scale, out,

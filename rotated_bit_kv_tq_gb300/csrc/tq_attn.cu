@@ -524,6 +524,14 @@ size_t attn_workspace_bytes(int n_seqs, int n_q_heads, int head_dim, int64_t max
     return kGridBarrierBytes + (grid ? 2 : 1) * rows;
 }
 
+size_t attn_need_bytes(const tq_cache &k, const tq_cache &v, int n_seqs, int n_q_heads, int64_t max_seq_len) {
+    const int sms = device_sm_count();
+    if (attn_t4_supported(k, v, n_q_heads) &&
+        !attn_t4_merges_itself(k, n_seqs, plan_splits(n_seqs, k.head_dim, max_seq_len, sms).n_splits))
+        return attn_t4_workspace_bytes(n_seqs, n_q_heads, k.head_dim, sms);
+    return attn_workspace_bytes(n_seqs, n_q_heads, k.head_dim, max_seq_len, sms);
+}
+
 tq_status launch_attn(const tq_cache &k, const tq_cache &v, const void *q, int n_seqs,
                       int n_q_heads, const int32_t *seq_lens, int64_t max_seq_len, float scale,
                       OutPtr out, void *ws, size_t ws_bytes, cudaStream_t stream,
@@ -549,9 +557,10 @@ tq_status launch_attn(const tq_cache &k, const tq_cache &v, const void *q, int n
     p.tokens_per_split = pl.tokens_per_split;
     const int Rk16 = (p.kc.row_bytes + 15) & ~15, Rv16 = (p.vc.row_bytes + 15) & ~15;
     p.tile_tokens = std::max(1, std::min(32, kTileBudget / (Rk16 + Rv16)));
-    if (ws_bytes < attn_workspace_bytes(n_seqs, n_q_heads, k.head_dim, max_seq_len,
-                                        device_sm_count()))
-        return TQ_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < attn_need_bytes(k, v, n_seqs, n_q_heads, max_seq_len)) return TQ_ERR_WORKSPACE_TOO_SMALL;
+    if (attn_t4_supported(k, v, n_q_heads))
+        return launch_attn_t4(k, v, q, n_seqs, n_q_heads, seq_lens, max_seq_len, scale, out, ws,
+                              p.n_splits, k_new, v_new, stream);
     if (attn_mma_supported(k, v, n_q_heads)) {
         // One wave of CTAs merges its own partials after a grid barrier (no merge kernel, no
         // kernel boundary before the output); otherwise a single sequence pairs its splits
@@ -615,8 +624,7 @@ extern "C" tq_status tq_attn_decode_noalloc(const tq_cache *k, const tq_cache *v
                                    softmax_scale, out, &scale);
     if (st != TQ_OK) return st;
     // The shape must fit the fixed array; larger shapes are refused, never truncated.
-    const size_t need = attn_workspace_bytes(n_seqs, n_q_heads, k->head_dim, max_seq_len,
-                                             device_sm_count());
+    const size_t need = attn_need_bytes(*k, *v, n_seqs, n_q_heads, max_seq_len);
     if (need > kStaticScratchBytes) return TQ_ERR_WORKSPACE_TOO_SMALL;
     void *scratch = nullptr;
     st = scratch_address(&scratch);

@@ -10,6 +10,16 @@ namespace {
 // Launches still to run with injected timeouts (tq_inject_wait_timeout).
 std::atomic<int> g_inject_timeouts{0};
 
+}  // namespace
+
+bool take_injected_timeout() {
+    for (int n = g_inject_timeouts.load(); n > 0;)
+        if (g_inject_timeouts.compare_exchange_weak(n, n - 1)) return true;
+    return false;
+}
+
+namespace {
+
 template <int NB>
 tq_status launch_nb(int tk, int tv, const MmaParams &p, int n_seqs, cudaStream_t stream) {
     if (tk == TQ_TURBO4 || tv == TQ_TURBO4) return launch_attn_mma_t4(tk, tv, NB, &p, n_seqs, stream);
@@ -80,12 +90,10 @@ tq_status launch_attn_mma(const tq_cache &k, const tq_cache &v, const void *q, i
     p.bar = bar;
     p.grid_wait_limit = kGridWaitLimit;
     if (out.p && (cluster != 1 || !bar || !grid_merge_fits(n_seqs, n_splits))) return TQ_ERR_UNSUPPORTED;
-    for (int n = g_inject_timeouts.load(); n > 0;)
-        if (g_inject_timeouts.compare_exchange_weak(n, n - 1)) {
-            p.wait_limit = kInjectedWaitLimit;
-            p.withhold_tiles = 1;
-            break;
-        }
+    if (take_injected_timeout()) {
+        p.wait_limit = kInjectedWaitLimit;
+        p.withhold_tiles = 1;
+    }
     p.mul2 = 2u;
     p.mul4 = 4u;
     p.hi16 = 1u << 16;

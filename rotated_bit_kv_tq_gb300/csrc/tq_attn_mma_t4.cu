@@ -1,5 +1,6 @@
 // tq_attn_mma_t4.cu -- tensor-core decode attention over pairs with one turbo4 cache (mixed
-// "-ctk" / "-ctv"); the kernel is tq_attn_mma_kernel.cuh's.
+// "-ctk" / "-ctv"); the kernel is tq_attn_mma_kernel.cuh's.  Two turbo4 caches run on
+// tq_attn_t4.cu.
 #include "tq_attn_mma_kernel.cuh"
 
 namespace tq {
@@ -7,7 +8,6 @@ namespace {
 
 template <int NB>
 tq_status launch_nb(int tk, int tv, const MmaParams &p, int n_seqs, cudaStream_t stream) {
-    if (tk == TQ_TURBO4 && tv == TQ_TURBO4) return launch_t<TQ_TURBO4, TQ_TURBO4, NB>(p, n_seqs, stream);
     if (tk == TQ_TURBO4)
         return tv == TQ_TURBO3 ? launch_t<TQ_TURBO4, TQ_TURBO3, NB>(p, n_seqs, stream)
                                : launch_t<TQ_TURBO4, TQ_TURBO2, NB>(p, n_seqs, stream);

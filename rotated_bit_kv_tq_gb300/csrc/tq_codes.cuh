@@ -138,10 +138,15 @@ __device__ __forceinline__ void e4m3x8(uint32_t W, uint32_t &lo, uint32_t &hi) {
     lo = prmt(kE4m3Lo4, kE4m3Hi4, sel) | (W & 0x80808080u);
     hi = prmt(kE4m3Lo4, kE4m3Hi4, sel >> 16) | ((W << 4) & 0x80808080u);
 }
-// Two e4m3 numbers (bits 0-15) as an fp16 pair; exact.
+// Two e4m3 numbers, bits 0-15 or 16-31 of x, as an fp16 pair; exact.
 __device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t x) {
     uint32_t d;
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(x));
+    return d;
+}
+__device__ __forceinline__ uint32_t e4m3_to_half2_hi(uint32_t x) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(d) : "r"(x));
     return d;
 }
 // `row` is a 16-byte aligned packed row in shared memory; ow / ov are the word-aligned
@@ -178,9 +183,9 @@ __device__ __forceinline__ void group_pairs(const Quarter<TYPE> &qw, int ww, int
         uint32_t lo, hi;
         e4m3x8(qw.w[2 * ww + r], lo, hi);
         o[0] = e4m3_to_half2(lo);
-        o[1] = e4m3_to_half2(lo >> 16);
+        o[1] = e4m3_to_half2_hi(lo);
         o[2] = e4m3_to_half2(hi);
-        o[3] = e4m3_to_half2(hi >> 16);
+        o[3] = e4m3_to_half2_hi(hi);
     } else {
     pairs8(t, sel8<TYPE>(ww ? qw.W1 : qw.W0, qw.V, r, 2 * ww + r, k), k.hi16, o);
     }

@@ -279,6 +279,8 @@ tq_status launch_decode(const tq_cache &src, int32_t seq_id, int64_t pos0, int64
                         float *dst, cudaStream_t stream);
 size_t attn_workspace_bytes(int n_seqs, int n_q_heads, int head_dim, int64_t max_seq_len,
                             int sm_count);
+// What a call on these caches needs (attn_workspace_bytes, or what tq_attn_t4.cu's batches need).
+size_t attn_need_bytes(const tq_cache &k, const tq_cache &v, int n_seqs, int n_q_heads, int64_t max_seq_len);
 // k_new / v_new (fp16 [n_seqs][Hkv][D], or null): append sequence s's new token at position
 // seq_lens[s] - 1 before attending (the tensor-core kernel does it in the same launch).
 tq_status launch_attn(const tq_cache &k, const tq_cache &v, const void *q, int n_seqs,
@@ -307,6 +309,15 @@ tq_status launch_attn_mma_t4(int tk, int tv, int nb, const void *params, int n_s
 
 // Fault injection of tq_inject_wait_timeout (tq_attn_mma.cu).
 tq_status inject_wait_timeout(int n_calls);
+bool take_injected_timeout();   // true for a launch that is to run out of its waits
+
+// Single-token attention over turbo4 K and V (tq_attn_t4.cu).
+bool attn_t4_supported(const tq_cache &k, const tq_cache &v, int n_q_heads);
+bool attn_t4_merges_itself(const tq_cache &k, int n_seqs, int n_splits);
+size_t attn_t4_workspace_bytes(int n_seqs, int n_q_heads, int head_dim, int sm_count);
+tq_status launch_attn_t4(const tq_cache &k, const tq_cache &v, const void *q, int n_seqs, int n_q_heads,
+                         const int32_t *seq_lens, int64_t max_seq_len, float scale, OutPtr out, void *ws,
+                         int n_splits, const void *k_new, const void *v_new, cudaStream_t stream);
 
 // Prompt-chunk attention on the 5th-generation tensor cores (tq_prefill_tc.cu).
 bool prefill_supported(const tq_cache &k, const tq_cache &v, int n_q_heads);
