@@ -100,6 +100,27 @@ def test_encode_bits_and_decode(tq, n, hkv, d, signs, correct):
     assert (out[:4] == 7).all() and (out[4 + n:] == 7).all()
 
 
+@pytest.mark.parametrize("hkv,off", [(8, 4), (3, 4), (8, 0)])
+def test_decode_offset_output_and_missing_rows(tq, hkv, off):
+    """An output on an odd 16-byte boundary; rows past the capacity read as zeros and are reported."""
+    r = rng(6, hkv, off)
+    n, over = 37, 5
+    x = kv16(r, n, hkv, 128).reshape(n, -1)
+    cache = tq.KVCache(tq.TQ_TURBO4, hkv, 128, capacity_tokens=n)
+    tq.encode(cache, dev(x))
+    flat = torch.full((off + (n - 2 + over) * hkv * 128 + 8,), 7.0, device=DEV)
+    out = flat[off:off + (n - 2 + over) * hkv * 128].view(-1, hkv, 128)
+    tq.decode(cache, 0, 2, n - 2 + over, out)
+    torch.cuda.synchronize()
+    assert tq.device_status() == 7
+    rows = ref.encode_rows(x, hkv)
+    got = out.cpu().numpy().astype(np.float64)
+    norms = ref.unpack(rows, hkv)[1][2:]
+    assert (np.abs(got[: n - 2] - ref.dequant(rows, hkv)[2:]) <= 10 * 2.0 ** -24 * 2.72 * norms[..., None]).all()
+    assert (got[n - 2:] == 0).all()
+    assert (flat[:off] == 7).all() and (flat[off + (n - 2 + over) * hkv * 128:] == 7).all()
+
+
 @pytest.mark.parametrize("n", [5, 900])
 def test_encode_kv_scattered_strided_paged(tq, n):
     """K and V of one call, token rows wider than the heads, positions in random order over
