@@ -507,7 +507,9 @@ tq_status launch_attn_t(const AttnParams &p, int n_seqs, cudaStream_t stream) {
 template <int TK>
 tq_status launch_attn_k(int tv, const AttnParams &p, int n_seqs, cudaStream_t stream) {
     switch (tv) {
-        case TQ_TURBO4: return launch_attn_t<TK, TQ_TURBO4>(p, n_seqs, stream);
+        case TQ_TURBO4:   // two turbo4 caches are launch_attn_t4's
+            if constexpr (TK == TQ_TURBO4) return TQ_ERR_UNSUPPORTED;
+            else return launch_attn_t<TK, TQ_TURBO4>(p, n_seqs, stream);
         case TQ_TURBO3: return launch_attn_t<TK, TQ_TURBO3>(p, n_seqs, stream);
         default: return launch_attn_t<TK, TQ_TURBO2>(p, n_seqs, stream);
     }

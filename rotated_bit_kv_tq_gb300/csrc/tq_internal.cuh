@@ -321,6 +321,7 @@ tq_status launch_attn_t4(const tq_cache &k, const tq_cache &v, const void *q, in
 
 // Prompt-chunk attention on the 5th-generation tensor cores (tq_prefill_tc.cu).
 bool prefill_supported(const tq_cache &k, const tq_cache &v, int n_q_heads);
+tq_status launch_prefill_t4(const void *params, int64_t n_ctas, cudaStream_t stream);   // tq_prefill_t4.cu
 tq_status launch_prefill(const tq_cache &k, const tq_cache &v, const void *q, int32_t seq_id,
                          int64_t pos0, int64_t n_q, int n_q_heads, float scale, OutPtr out,
                          cudaStream_t stream);
