@@ -166,7 +166,7 @@ __device__ __forceinline__ void for_segments(const T4Params &p, int64_t c, int64
     const int lane = threadIdx.x & 31;
     if (p.n_seqs == 1) {
         const int len = clamped_len(p, p.seq_lens[0]);
-        const int chunk = max(kMinChunk, (len + (int)n_chunks - 1) / (int)n_chunks);
+        const int chunk = max(kMinChunk, (int)((len + n_chunks - 1) / n_chunks));
         const int64_t lo = c * chunk;
         f(0, len, (int)min64(lo, len), (int)min64(lo + chunk, len), int64_t(0), (int64_t)chunk);
         return;
@@ -175,7 +175,7 @@ __device__ __forceinline__ void for_segments(const T4Params &p, int64_t c, int64
     for (int i = lane; i < p.n_seqs; i += 32) {
         const int len = p.seq_lens[i];
         const int l = len < 0 ? 0 : min(len, p.max_len);
-        total += l > 0 ? l + kSegPad : 0;
+        total += l > 0 ? (int64_t)l + kSegPad : 0;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -192,7 +192,7 @@ __device__ __forceinline__ void for_segments(const T4Params &p, int64_t c, int64
                 len = len < 0 ? 0 : p.max_len;
             }
         }
-        int64_t x = len > 0 ? len + kSegPad : 0;
+        int64_t x = len > 0 ? (int64_t)len + kSegPad : 0;
         const int64_t mine = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1003,7 +1003,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_t4_merge_kernel(const _
     const int h = blockIdx.x, seq = blockIdx.y, b = blockIdx.z;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t at = ((int64_t)seq * p.n_q_heads + h) * D + b * kBlock + 4 * lane;
-    if (p.seq_lens[seq] <= 0) {
+    if (min(p.seq_lens[seq], p.max_len) <= 0) {   // no chunk holds rows of it
         if (warp == 0) store_out4(p.out, at, 0.f, 0.f, 0.f, 0.f);
         return;
     }

@@ -44,7 +44,7 @@ namespace {
 // P1 [448,512) fp16 pairs (the A operand of P V)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256, kTmemP = 384;
-constexpr float kVDown4 = 0.015625f;   // turbo4 V norms in the fp16 tile: |v| c <= 12288
+constexpr float kVDown4 = 0.0625f;   // turbo4 V norms in the fp16 tile: |v| c <= 49,128
 
 // mbarriers
 // Buffer b of a double-buffered resource serves tiles b, b + 2, ...; a waiter for tile i
