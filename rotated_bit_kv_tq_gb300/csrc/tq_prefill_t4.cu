@@ -8,8 +8,9 @@
 //
 //  - Warps 0-3 take the even tiles, warps 4-7 the odd ones, and each of the two groups has its own
 //    running maximum, sum and output accumulator.  Nothing passes between them until the end, so
-//    one group's softmax runs while the other waits for its products.  (All eight warps on one
-//    tile, exchanging row maxima for every tile: 531 us; two groups of eight warps: 590 us.)
+//    one group's softmax runs while the other waits for its products.  (Measured before the later steps, at 518 us: all eight
+//    warps on one tile, exchanging row maxima for every tile, 531 us; two groups of eight warps
+//    590 us.)
 //  - Warps 8-11 (K) and 12-15 (V), one thread per key: stage the tile's codes (cp.async, four
 //    lanes per key so that a request covers whole 32-byte sectors) and expand them once to fp16.
 //  - Warp 16 issues the MMAs: S = Q~ C^T with Q~ as an fp16 pair hi + lo, and O += P V.
@@ -28,12 +29,12 @@
 // The rotation Q~ = H D q is a product as well: the signs of D go into a +-1 matrix, and the
 // sums of fp16 queries are exact up to the fp32 accumulator's rounding.
 //
-// What bounds it: 1,024 queries of 32 heads over 15,360 rows of 8 KV heads take 489 us, 3,600 clocks
-// per tile, of which the MMAs need 1,536 (the score MMAs twice, for the query's low parts) and
-// what they read from shared memory 1,280; the rest of shared memory's time is the tiles written
-// (512), the staged codes and the norms.  A group's chain for one tile is 1,400 clocks of score
-// MMAs, 3,800 of softmax and 1,800 until its next scores can start; without any softmax
-// arithmetic the kernel took 408 us.
+// What bounds it: 1,024 queries of 32 heads over 15,360 rows of 8 KV heads take 467 us (39 % of the
+// tensor cores' cycles, 49 % of the issue slots), in two waves of which the second fills 104 of
+// 152 SMs.  A tile takes 3,400 clocks, of which the MMAs need 1,536 (the score MMAs twice, for
+// the query's low parts) and what they read from shared memory 1,280; the tiles written, the
+// staged codes and the norms take another 1,000 of shared memory's time.  A group's chain for one
+// tile is 1,400 clocks of score MMAs, 3,500 of softmax and 1,700 until its next scores can start.
 #include <cmath>
 
 #include "tq_prefill_tc.cuh"
@@ -182,45 +183,43 @@ __device__ __forceinline__ void p4_produce(const TcParams &p, P4Smem &sm, int g,
         const int b = i & 1;
         cp_async_wait<0>();
         __syncwarp();
-        uint32_t n[16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(raw + code_chunk(pt, c));
-            n[4 * c] = u.x, n[4 * c + 1] = u.y, n[4 * c + 2] = u.z, n[4 * c + 3] = u.w;
-        }
-        const uint32_t nb = nrm, vb = vnrm;
-        __syncwarp();   // the warp has read its codes
-        if (i + 1 < n_tiles) stage();
         if (i >= 2 && !*abort_v && !tc_wait(smem_u32(&sm.bar[wait_bar + b]), (uint32_t)(((i - 2) >> 1) & 1)))
             *abort_v = 1;
         uint8_t *tile = IS_V ? sm.v[b] : sm.k[b];
         __half2 u2 = __half2half2(__ushort_as_half(0));
         if (IS_V) {
-            u2 = __half2half2(v_scale(nb));
+            u2 = __half2half2(v_scale(nrm));
         } else {
-            sm.kn[i & 3][pt] = __half2float(__ushort_as_half((uint16_t)nb));
-            const float u = __half2float(v_scale(vb));
-            sm.vr[i & 3][pt] = u != 0.f ? __half2float(__ushort_as_half((uint16_t)vb)) / u : 0.f;
+            sm.kn[i & 3][pt] = __half2float(__ushort_as_half((uint16_t)nrm));
+            const float u = __half2float(v_scale(vnrm));
+            sm.vr[i & 3][pt] = u != 0.f ? __half2float(__ushort_as_half((uint16_t)vnrm)) / u : 0.f;
         }
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {   // a quarter at a time: unrolled in full, 476 us instead of 467: instruction caches
+            const uint4 x = *reinterpret_cast<const uint4 *>(raw + code_chunk(pt, c));
+            const uint32_t n[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            uint32_t lo, hi, o[4];
-            e4m3x8(n[w], lo, hi);
-            o[0] = e4m3_to_half2(lo);
-            o[1] = e4m3_to_half2_hi(lo);
-            o[2] = e4m3_to_half2(hi);
-            o[3] = e4m3_to_half2_hi(hi);
-            if (IS_V)
+            for (int w = 0; w < 4; ++w) {
+                uint32_t lo, hi, o[4];
+                e4m3x8(n[w], lo, hi);
+                o[0] = e4m3_to_half2(lo);
+                o[1] = e4m3_to_half2_hi(lo);
+                o[2] = e4m3_to_half2(hi);
+                o[3] = e4m3_to_half2_hi(hi);
+                if (IS_V)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[e]), u2);
-                    o[e] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-            *reinterpret_cast<uint4 *>(tile + (IS_V ? canon_mn(pt, 8 * w) : canon(pt, 8 * w))) = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&o[e]), u2);
+                        o[e] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                const int at = 32 * c + 8 * w;
+                *reinterpret_cast<uint4 *>(tile + (IS_V ? canon_mn(pt, at) : canon(pt, at))) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) tc_arrive(smem_u32(&sm.bar[full_bar + b]));
+        if (i + 1 < n_tiles) stage();   // the warp has read its codes
     }
     cp_async_wait<0>();
 }
@@ -605,7 +604,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_t4_kernel(const TcParam
             ok = __all_sync(0xffffffffu, tc_wait(bar(kP4BarQ), 0));
         }
         // S(0), S(1), then P V(i) and S(i + 2) in turn, with blocking waits: a warp that polled for
-        // whichever came first took issue slots from the softmax (513 us where this takes 489)
+        // whichever came first took issue slots from the softmax (513 us against 489 at the time)
         auto wait = [&](int first, int i) {
             if (ok && !__all_sync(0xffffffffu, tc_wait(bar(first + (i & 1)), (uint32_t)((i >> 1) & 1)) && !*abort_v)) ok = false;
         };
@@ -671,8 +670,8 @@ tq_status launch_prefill_t4(const void *params, int64_t n_ctas, cudaStream_t str
     // The key tiles of a query block over a cluster of 1, 2 or 4 CTAs, whichever ends first by the
     // count of waves times the tiles of a CTA and what a CTA spends around them (the queries'
     // rotation, the ends of the pipeline, the epilogue, the cluster's waits: about kAround
-    // tiles).  1, 2, 4 CTAs take 40.6, 26.5, 19.0 us for 49 queries of 40 heads over 1,000 rows
-    // and 489, 510, 549 us for 1,024 queries of 32 heads over 15,360; clusters of 8 took 32 and
+    // tiles).  1, 2, 4 CTAs take 38.7, 25.5, 18.1 us for 49 queries of 40 heads over 1,000 rows
+    // and 467, 490, 530 us for 1,024 queries of 32 heads over 15,360; clusters of 8 took 32 and
     // 756 us, since 8 free SMs of one processing cluster are rare.
     const int64_t sms = device_sm_count();
     const int64_t tiles = (p.pos0 + p.n_q + kTcKeys - 1) / kTcKeys;
