@@ -82,17 +82,19 @@ __global__ void __launch_bounds__(256) decode_kernel(const DecodeParams p) {
 
 // ------------------------------------------------------------------ turbo4
 // W is a tensor product over the seven bits of the coordinate.  A warp takes 16 blocks; four of
-// the bits (0, 1, 5, 6) are summed by m16n8k16 products with a 16 x 16 matrix of +-1, the other
-// three (2, 3, 4) by butterflies between the eight k-steps' accumulators:
-//   A[block][k]: lane (g, q) holds the 16-byte code chunk q (bits 5, 6) of blocks g and g + 8; its
-//       word (bits 3, 4) and half word (bit 2) number the k-steps, its four values (bits 0, 1)
-//       and q are the k of one step, as exact fp16 numbers;
-//   B[k][n] = +-1 for output bits 0 (n & 1), 5, 6 (n >> 1) and 1 (which of two n-tiles).
+// the bits (0, 1, 3, 4) are summed by m16n8k16 products with a 16 x 16 matrix of +-1, the other
+// three (2, 5, 6) by butterflies between the eight k-steps' accumulators:
+//   A[block][k]: lane (g, q) holds word q (bits 3, 4) of each 16-byte code chunk of blocks g and
+//       g + 8; the chunk (bits 5, 6) and half word (bit 2) number the k-steps, the four values
+//       (bits 0, 1) and q are the k of one step, as exact fp16 numbers;
+//   B[k][n] = +-1 for output bits 0 (n & 1), 3, 4 (n >> 1) and 1 (which of two n-tiles).
 // The sums are whole multiples of 1/16 below 2^11: exact in fp32, so the result has one rounding
-// (times the norm).  Lane (g, q) ends with coordinates 32 q + 0 .. 31 of its blocks: 32-byte
-// stores.  17 instructions per block and warp against about 170 in the shuffle form, which took
-// 127 us for the 32,768 x 8 blocks of a Llama-shape cache; the output's 4 bytes per value are
-// the bound.
+// (times the norm).  Lane (g, q) ends with coordinates 32 e + 8 q + 0 .. 7 of its blocks, so the
+// four lanes of a block store whole 128-byte lines (with 32 consecutive coordinates per lane each
+// store touched 32 lines: 36.7 us where this took 32.2).
+// The 32,768 x 8 blocks of a Llama-shape cache take 28.2 us, 5.4 TB/s of codes read and fp32
+// written (floor 22.4); 127 us in the shuffle form above.  Four CTAs of four warps per SM: three
+// take 29.6 us, five 29.5.
 // (two 16-byte stores where the output starts on an odd 16-byte boundary)
 __device__ __forceinline__ void store8(float *p, const float (&v)[8], bool wide) {
     if (!wide) {
@@ -106,7 +108,7 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8], bool wide)
 
 constexpr int kDecodeWarps = 4;
 
-// One lane's share of a tile: the code chunks q4 of blocks g8 and g8 + 8, their scales, and what
+// One lane's share of a tile: words q4 of the code chunks of blocks g8 and g8 + 8, their scales, and what
 // becomes of them.
 struct DecodeTile {
     uint32_t w[2][4];
@@ -122,33 +124,31 @@ __device__ __forceinline__ void decode_load(const DecodeParams &p, int64_t tile,
 #pragma unroll
         for (int e = 0; e < 4; ++e) d.w[r][e] = 0u;
         if (blk >= p.n_blocks) continue;
-        const int64_t t = blk / p.bpr;
+        const int64_t t = blk >> 32 ? blk / p.bpr : (int64_t)((uint32_t)blk / (uint32_t)p.bpr);
         const int fb = (int)(blk - t * p.bpr);
         const uint8_t *row = row_ptr(p.src, p.seq_id, p.pos0 + t);
         if (!row) continue;   // a row outside the cache reads as zeros
         d.present[r] = true;
-        const uint8_t *c = row + fb * kCodeBytes4 + 16 * q4;
-        if (p.src.row_bytes % 16 == 0) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(c);
-            d.w[r][0] = u.x, d.w[r][1] = u.y, d.w[r][2] = u.z, d.w[r][3] = u.w;
-        } else {
+        const uint8_t *c = row + fb * kCodeBytes4 + 4 * q4;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                d.w[r][e] = reinterpret_cast<const uint16_t *>(c)[2 * e] | (uint32_t)reinterpret_cast<const uint16_t *>(c)[2 * e + 1] << 16;
-        }
+        for (int e = 0; e < 4; ++e)
+            if (p.src.row_bytes % 4 == 0)
+                d.w[r][e] = *reinterpret_cast<const uint32_t *>(c + 16 * e);
+            else
+                d.w[r][e] = *reinterpret_cast<const uint16_t *>(c + 16 * e) | (uint32_t)*reinterpret_cast<const uint16_t *>(c + 16 * e + 2) << 16;
         d.norm[r] = *reinterpret_cast<const __half *>(row + norm_offset(TQ_TURBO4, fb, p.bpr));
     }
 }
 
 // A warp takes every n-th tile and has the next one's codes in flight while it works.
-__global__ void __launch_bounds__(32 * kDecodeWarps, 5) decode4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(32 * kDecodeWarps, 4) decode4_kernel(const DecodeParams p) {
     const int lane = threadIdx.x & 31, g8 = lane >> 2, q4 = lane & 3;
     const int64_t step = (int64_t)gridDim.x * kDecodeWarps, n_tiles = (p.n_blocks + 15) / 16;
     const bool wide = reinterpret_cast<uintptr_t>(p.dst) % 32 == 0;
     pdl_wait();
     pdl_launch_dependents();
-    // B fragments: column n = g8 is output (bit 0 = g8 & 1, bits 5-6 = g8 >> 1); row k is input
-    // (bits 5-6 = q4, bits 0-1 = e), b0: e = 0, 1, b1: e = 2, 3; the second n-tile is output bit 1
+    // B fragments: column n = g8 is output (bit 0 = g8 & 1, bits 3-4 = g8 >> 1); row k is input
+    // (bits 3-4 = q4, bits 0-1 = e), b0: e = 0, 1, b1: e = 2, 3; the second n-tile is output bit 1
     const uint32_t flip = (__popc(q4 & (g8 >> 1)) & 1) ? 0x80008000u : 0u;
     const uint32_t b0 = (0x3C003C00u | ((g8 & 1) ? 0x80000000u : 0u)) ^ flip, b1 = b0 ^ 0x80008000u;
     int64_t tile = (int64_t)blockIdx.x * kDecodeWarps + (threadIdx.x >> 5);
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, 5) decode4_kernel(const Dec
     for (; tile < n_tiles; tile += step) {
         const DecodeTile cur = next;
         if (tile + step < n_tiles) decode_load(p, tile + step, g8, q4, next);
-        float d[8][2][4];   // [k-step: bit 2 + 2 (bits 3-4)][output bit 1][row g8: bit 0; row g8 + 8: bit 0]
+        float d[8][2][4];   // [k-step: bit 2 + 2 (bits 5-6)][output bit 1][row g8: bit 0; row g8 + 8: bit 0]
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             uint32_t xl, xh, yl, yh;
@@ -192,20 +192,20 @@ __global__ void __launch_bounds__(32 * kDecodeWarps, 5) decode4_kernel(const Dec
         for (int r = 0; r < 2; ++r) {
             if (tile * 16 + g8 + 8 * r >= p.n_blocks) continue;
             const float scale = __half2float(cur.norm[r]) * (kInvSqrt128 * kE4m3Step4);
-            float *out = p.dst + (tile * 16 + g8 + 8 * r) * kBlock + 32 * q4;
+            float *out = p.dst + (tile * 16 + g8 + 8 * r) * kBlock + 8 * q4;
             // rotation-sign variant: the inverse is D W
-            const uint32_t sg = cur.present[r] && p.src.has_signs ? (q4 == 0 ? p.src.signs[0] : q4 == 1 ? p.src.signs[1] : q4 == 2 ? p.src.signs[2] : p.src.signs[3]) : 0u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = __uint_as_float(__float_as_uint(d[2 * e + (i >> 2)][(i >> 1) & 1][2 * r + (i & 1)] * scale) ^
-                                           ((sg >> (8 * e + i)) << 31));
-                if (!cur.present[r])
+                for (int i = 0; i < 8; ++i)   // (+ 0: a missing row, scale 0, reads as +0)
+                    v[i] = fmaf(d[2 * e + (i >> 2)][(i >> 1) & 1][2 * r + (i & 1)], scale, 0.f);
+                if (p.src.has_signs) {
+                    const uint32_t sg = cur.present[r] ? p.src.signs[e] >> (8 * q4) : 0u;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                store8(out + 8 * e, v, wide);
+                    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(__float_as_uint(v[i]) ^ ((sg >> i) << 31));
+                }
+                store8(out + 32 * e, v, wide);
             }
         }
     }
@@ -225,8 +225,8 @@ tq_status launch_decode(const tq_cache &src, int32_t seq_id, int64_t pos0, int64
     const int64_t grid = (p.n_blocks + 7) / 8;
     if (grid > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
     if (src.type == TQ_TURBO4) {
-        // a wave of resident CTAs (five of four warps per SM)
-        const int64_t ctas = min64((p.n_blocks + 16 * kDecodeWarps - 1) / (16 * kDecodeWarps), (int64_t)5 * device_sm_count());
+        // a wave of resident CTAs (four of four warps per SM)
+        const int64_t ctas = min64((p.n_blocks + 16 * kDecodeWarps - 1) / (16 * kDecodeWarps), (int64_t)4 * device_sm_count());
         PdlConfig lc(dim3((unsigned)ctas), dim3(32 * kDecodeWarps), 0, stream);
         return check_cuda(cudaLaunchKernelEx(&lc.cfg, decode4_kernel, p));
     } else if (src.type == TQ_TURBO3)
