@@ -134,13 +134,6 @@ struct RowWalk {
     }
 };
 
-// u_t of a V norm: the power of two at or below it, at most 2^12; a norm below fp16's normal
-// range stays as it is.
-__device__ __forceinline__ __half v_scale(uint32_t bits) {
-    const uint32_t b = bits & 0xfc00u;
-    return __ushort_as_half((uint16_t)((b & 0x7c00u) > 0x6c00u ? 0x6c00u : b & 0x7c00u ? b : bits));
-}
-
 // One producer group, one thread per key: stage and expand every tile of its cache.  A warp
 // stages the rows of its own 32 keys, so it needs no barrier beyond its own.
 template <bool IS_V>
@@ -660,7 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_t4_kernel(const TcParam
 
 }  // namespace
 
-// p is complete but for out_scale's turbo4 tile factor (none here) and split.
+// params: a TcParams, complete but for split.
 tq_status launch_prefill_t4(const void *params, int64_t n_ctas, cudaStream_t stream) {
     TcParams p = *static_cast<const TcParams *>(params);
     const size_t smem = sizeof(P4Smem) + 1024;   // room to align the tiles to 1024 bytes

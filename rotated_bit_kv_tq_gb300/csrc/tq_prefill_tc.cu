@@ -192,10 +192,11 @@ __device__ __forceinline__ void tc_decode(const uint32_t (&n)[win_words(TYPE)], 
     // (|v| c); K keeps it apart (norm[]) and the scores are scaled in fp32, which keeps one
     // fp16 rounding on the score path
     // turbo4's operands reach 12, so its V norms are taken down by kVDown4 (an exact scaling
-    // of all but subnormal results), which the output scale undoes
+    // of all but subnormal results), which the output scale undoes; at head_dim 256 the operand
+    // takes a power of two and the weights the rest (v_scale)
     constexpr int kNormWord = TYPE == TQ_TURBO4 ? 16 : 0;
     const __half nrm = present ? __ushort_as_half((uint16_t)(n[kNormWord] & 0xffffu)) : __ushort_as_half(0);
-    const __half nsc = TYPE == TQ_TURBO4 && MN ? __hmul(nrm, __float2half_rn(kVDown4)) : nrm;
+    const __half nsc = TYPE != TQ_TURBO4 || !MN ? nrm : NC == 128 ? __hmul(nrm, __float2half_rn(kVDown4)) : v_scale(__half_as_ushort(nrm));
     const __half2 n2 = __halves2half2(nsc, nsc);
     if (!MN) norm[pt] = __half2float(nrm);
 #pragma unroll
@@ -650,12 +651,15 @@ struct TcSmem256 {
     alignas(1024) uint8_t ql[65536];       // Q~ low parts [row][coord 0..255], K-major
     alignas(1024) uint8_t k[2][2][16384];  // [buffer][block] K tile [key][coord], K-major
     alignas(1024) uint8_t v[32768];        // V tile [key][coord 0..255], MN-major
-    alignas(1024) uint8_t p[2][16384];     // [buffer] P [row][key] fp16, K-major
+    alignas(1024) uint8_t p[2][16384];     // [buffer; turbo4 V: block] P [row][key] fp16, K-major
     alignas(16) uint8_t raw_k[2][k2Keys * 64];   // staged K blocks (64-byte key windows)
     alignas(16) uint8_t raw_v[2][k2Keys * 64];   // staged V blocks
     // [tile mod 3][block][key] norms: the producer writes tile i + 2's norms once tile i's
     // score MMAs are done, possibly before the softmax has read tile i's
     float kn[3][2][k2Keys];
+    // [tile mod 4][block][key] turbo4: what the weights take of the V norms (read after the scores
+    // have been given back, so one tile longer than the key norms)
+    float vr[4][2][k2Keys];
     float xch[2][2][kTcRows];
     uint8_t ok[4][k2Keys];                 // K block 0, K block 1, V block 0, V block 1
     alignas(8) uint64_t bar[k2BarCount];
@@ -697,6 +701,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
     const int64_t first_pos = p.pos0 + j0;
     const int n_tiles = (int)((n_keys + k2Keys - 1) / k2Keys);
     constexpr int D = 2 * kBlock;
+    // turbo4 V: each block has its own weights, p times what its V operand leaves of the norm, so that
+    // a product has one rounding; both blocks' weights together are one tile's, in place of two
+    // tiles' buffers
+    constexpr bool kOwnP = TV == TQ_TURBO4;
     auto bar = [&](int i) { return smem_u32(&sm.bar[i]); };
 
     if (tid == 0) {
@@ -827,24 +835,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
                 alpha = m_run == -INFINITY ? 0.f : ex2(m_run - mx);
                 m_run = mx;
             }
-            // P buffer b is free once tile i - 2's P V is done
-            if (i >= 2 && !*abort_v && !tc_wait(bar(k2BarPvFree + b), (uint32_t)(((i - 2) >> 1) & 1)))
+            // P buffer b is free once tile i - 2's P V is done (the blocks' weights: tile i - 1's)
+            constexpr int kBack = kOwnP ? 1 : 2;
+            if (i >= kBack && !*abort_v &&
+                !tc_wait(bar(k2BarPvFree + ((i - kBack) & 1)), (uint32_t)(((i - kBack) >> 1) & 1)))
                 *abort_v = 1;
             tc_fence_after();
             float ps8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const float mref = m_run == -INFINITY ? 0.f : m_run;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {   // keys 32 h + 8 c .. + 7 of row r
-                uint32_t w[4];
+                if constexpr (kOwnP) {
+                    uint32_t w0[4], w1[4];
+                    const float *v0 = sm.vr[i & 3][0] + 32 * h + 8 * c, *v1 = sm.vr[i & 3][1] + 32 * h + 8 * c;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 8 * c + 2 * e;
-                    const float p0 = ex2(s[j] - mref), p1 = ex2(s[j + 1] - mref);
-                    ps8[j & 7] += p0;
-                    ps8[(j + 1) & 7] += p1;
-                    w[e] = pack_half2(p0, p1);
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 8 * c + 2 * e;
+                        const float p0 = ex2(s[j] - mref), p1 = ex2(s[j + 1] - mref);
+                        ps8[j & 7] += p0;
+                        ps8[(j + 1) & 7] += p1;
+                        // (a masked key's share of the norm may be anything)
+                        w0[e] = pack_half2(p0 == 0.f ? 0.f : p0 * v0[2 * e], p1 == 0.f ? 0.f : p1 * v0[2 * e + 1]);
+                        w1[e] = pack_half2(p0 == 0.f ? 0.f : p0 * v1[2 * e], p1 == 0.f ? 0.f : p1 * v1[2 * e + 1]);
+                    }
+                    *reinterpret_cast<uint4 *>(sm.p[0] + canon64(r, 32 * h + 8 * c)) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                    *reinterpret_cast<uint4 *>(sm.p[1] + canon64(r, 32 * h + 8 * c)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 8 * c + 2 * e;
+                        const float p0 = ex2(s[j] - mref), p1 = ex2(s[j + 1] - mref);
+                        ps8[j & 7] += p0;
+                        ps8[(j + 1) & 7] += p1;
+                        w[e] = pack_half2(p0, p1);
+                    }
+                    *reinterpret_cast<uint4 *>(sm.p[b] + canon64(r, 32 * h + 8 * c)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                *reinterpret_cast<uint4 *>(sm.p[b] + canon64(r, 32 * h + 8 * c)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             const float psum = ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
             l_run = l_run * alpha + psum;
@@ -922,7 +949,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
         if (tid - kTcSoftmax < kTcGroup) {
             // K: double-buffered tiles, one 16 KB tile per block
             const HalfTables tab = make_tables<TK>();
-            uint32_t nrm = 0;
+            uint32_t nrm = 0, vnrm = 0;   // norm bits of the staged tile: K (turbo4), V (turbo4)
+            auto v_norm = [&](int64_t t) -> uint32_t {
+                const uint8_t *row = kOwnP && t < n_keys ? row_ptr(p.vc, p.seq, t) : nullptr;
+                return row ? *reinterpret_cast<const uint16_t *>(row + norm_offset(TV, 2 * g + blk, p.vc.row_bytes / block_bytes(TV))) : 0;
+            };
+            vnrm = v_norm(key);
             if (n_tiles > 0)
                 nrm = tc_stage<TK>(p.kc, p.seq, p.chunked_k, sm.raw_k[blk], sm.ok[blk], 2 * g + blk, 0, n_keys, key);
             cp_async_commit();
@@ -932,6 +964,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
                 uint32_t nb[win_words(TK)];
                 tc_window<TK>(sm.raw_k[blk], nrm, 2 * g + blk, key, nb);
                 const bool present = sm.ok[blk][key] != 0;
+                const uint32_t vb = vnrm;
+                if (i + 1 < n_tiles) vnrm = v_norm((int64_t)(i + 1) * k2Keys + key);
                 if (i + 1 < n_tiles)
                     nrm = tc_stage<TK>(p.kc, p.seq, p.chunked_k, sm.raw_k[blk], sm.ok[blk], 2 * g + blk,
                                  (int64_t)(i + 1) * k2Keys, n_keys, key);
@@ -939,6 +973,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
                 if (i >= 2 && !*abort_v && !tc_wait(bar(k2BarKFree + b), (uint32_t)(((i - 2) >> 1) & 1)))
                     *abort_v = 1;
                 tc_decode<TK, false>(nb, present, tab, sm.k[b][blk], sm.kn[i % 3][blk], key);
+                if (kOwnP) {
+                    const float u = __half2float(v_scale(vb));
+                    sm.vr[i & 3][blk][key] = u != 0.f ? __half2float(__ushort_as_half((uint16_t)vb)) / u : 0.f;
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_arrive(bar(k2BarKFull + b));
             }
@@ -1004,12 +1042,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc256_kernel(const TcPa
                 tc_test(bar(k2BarVFull), (uint32_t)(npv & 1))) {
                 tc_fence_after();
                 const int b = npv & 1;
-                const uint32_t p_base = smem_u32(sm.p[b]);
-                // A = P from shared memory (16 keys per MMA), B = the V tile, N = 256
+                // A = P from shared memory (16 keys per MMA), B = the V tile, N = 256 (or each block's, 128)
+                if constexpr (kOwnP) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc_mma(tmem + k2O, sdesc(p_base + 256u * kk, 128, 1024),
-                           sdesc(v_base + 8192u * kk, 4096, 128), idesc_pv, (npv > 0 || kk > 0));
+                    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma(tmem + k2O + 128u * blk, sdesc(smem_u32(sm.p[blk]) + 256u * kk, 128, 1024),
+                                   sdesc(v_base + 2048u * blk + 8192u * kk, 4096, 128), idesc_f16(true), (npv > 0 || kk > 0));
+                } else {
+                    const uint32_t p_base = smem_u32(sm.p[b]);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma(tmem + k2O, sdesc(p_base + 256u * kk, 128, 1024),
+                               sdesc(v_base + 8192u * kk, 4096, 128), idesc_pv, (npv > 0 || kk > 0));
+                }
                 tc_commit(bar(k2BarPvFree + b));
                 ++npv;
                 progressed = true;
@@ -1107,14 +1154,13 @@ tq_status launch_prefill(const tq_cache &k, const tq_cache &v, const void *q, in
     // the fp16 centroid tables are scaled by h_scale (Codebook); the query scale divides the
     // K table's out, the output scale the V table's
     p.score_scale = scale * kTcLog2e * kInvSqrt128 / centroid_h_scale(k.type);
-    p.out_scale = kInvSqrt128 / centroid_h_scale(v.type) / (v.type == TQ_TURBO4 ? kVDown4 : 1.0f);
+    p.out_scale = kInvSqrt128 / centroid_h_scale(v.type);
     p.n_kv_heads = k.n_kv_heads;
     p.n_qblocks = (n_q + p.bq - 1) / p.bq;
     const int64_t n_ctas = p.n_qblocks * k.n_kv_heads;
     if (n_ctas > 0x3fffffff) return TQ_ERR_UNSUPPORTED;
     if (k.head_dim == kBlock && k.type == TQ_TURBO4 && v.type == TQ_TURBO4) {
         if (n_ctas > (0x3fffffff >> 3)) return TQ_ERR_UNSUPPORTED;
-        p.out_scale = kInvSqrt128 / centroid_h_scale(v.type);   // its V tiles are not scaled down
         return launch_prefill_t4(&p, n_ctas, stream);
     }
     const unsigned nc = (unsigned)n_ctas;
@@ -1126,6 +1172,7 @@ tq_status launch_prefill(const tq_cache &k, const tq_cache &v, const void *q, in
             default: return launch_tc256_k<TQ_TURBO2>(v.type, p, nc, stream);
         }
     }
+    if (v.type == TQ_TURBO4) p.out_scale /= kVDown4;
     // Split each query block's key tiles over a cluster of two CTAs when that fills the last
     // wave of one-CTA-per-SM launches markedly better (the two CTAs both rotate the queries,
     // so a split costs a little): e.g. the 512 CTAs of a 2,048-token chunk of a Llama-shape

@@ -97,6 +97,14 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t local, uint32_t rank
     return v;
 }
 
+// The part u of a turbo4 V norm v that the V operand takes (u c is exact in fp16; the weights take
+// v / u): the power of two at or below v, at most 2^12; a norm below fp16's normal range stays as
+// it is.
+__device__ __forceinline__ __half v_scale(uint32_t bits) {
+    const uint32_t b = bits & 0xfc00u;
+    return __ushort_as_half((uint16_t)((b & 0x7c00u) > 0x6c00u ? 0x6c00u : b & 0x7c00u ? b : bits));
+}
+
 // In-thread Walsh-Hadamard butterflies over 64 values, h = 1 .. 32.
 __device__ __forceinline__ void fwht64(float (&x)[64]) {
 #pragma unroll

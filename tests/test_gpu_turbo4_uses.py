@@ -185,6 +185,44 @@ def test_later_rows_that_are_not_finite(tq, bad):
     expect(one, ks[0][:70], vs[0][:70], q[:1], hkv)
 
 
+@pytest.mark.parametrize("bad", [0x7C00, 0x7E00])
+@pytest.mark.parametrize("page", [0, 32])
+def test_later_rows_that_are_not_finite_head_dim_256(tq, bad, page):
+    r = rng(32, bad, page)
+    hkv, hq, d, n, nq = 2, 8, 256, 90, 40
+    blocks = hkv * 2
+    kc, vc, ks, vs = caches(tq, r, (n,), hkv, d, page)
+    for c in (kc, vc):
+        rows = c.buffer.view(-1, blocks * 66)
+        for t in range(70, n):
+            at = int(c.page_table[0, t // page]) * page + t % page if page else t
+            rows[at, blocks * 64:].view(torch.int16).copy_(torch.tensor(bad, dtype=torch.int16))
+    q = r.standard_normal((nq, hq, d)).astype(np.float16)
+    out = torch.empty(nq, hq, d, dtype=torch.float16, device=DEV)
+    tq.attn_prefill(kc, vc, dev(q), out, pos0=n - nq)       # queries 0 .. 19 see rows 0 .. 69
+    torch.cuda.synchronize()
+    assert tq.device_status() == 0
+    see = np.arange(70)[None] <= (n - nq + np.arange(20))[:, None]
+    expect(out[:20], ks[0][:70], vs[0][:70], q[:20], hkv, see, True)
+
+
+@pytest.mark.parametrize("power", [-4, 0, 4])
+def test_prompt_chunk_value_sizes_head_dim_256(tq, power):
+    """One rounding per product at every size of the values (test_prompt_chunk allows two)."""
+    r = rng(33, 9 + power)
+    hkv, hq, d, n, nq = 2, 8, 256, 200, 30
+    blocks = hkv * 2
+    ks = ref.encode_rows(kv16(r, n, hkv, d, True).reshape(n, -1), blocks, None)
+    vs = ref.encode_rows((kv16(r, n, hkv, d).astype(np.float32) * 10.0 ** power).astype(np.float16).reshape(n, -1), blocks, None)
+    kc, vc = (make_cache(tq, tq.TQ_TURBO4, hkv, d, [x]) for x in (ks, vs))
+    q = r.standard_normal((nq, hq, d)).astype(np.float16)
+    out = torch.empty(nq, hq, d, device=DEV)
+    tq.attn_prefill(kc, vc, dev(q), out, pos0=n - nq)
+    torch.cuda.synchronize()
+    assert tq.device_status() == 0
+    expect(out, ks, vs, q, hkv, np.arange(n)[None] <= (n - nq + np.arange(nq))[:, None])
+
+
 @pytest.mark.parametrize("page", [0, 256])
 def test_rows_past_four_gigabytes(tq, page):
     """A sequence whose rows start 4.4 GB into the pool: written, read back, attended to."""
