@@ -668,6 +668,7 @@ tq_status launch_prefill_t4(const void *params, int64_t n_ctas, cudaStream_t str
     // 756 us, since 8 free SMs of one processing cluster are rare.
     const int64_t sms = device_sm_count();
     const int64_t tiles = (p.pos0 + p.n_q + kTcKeys - 1) / kTcKeys;
+    if (tiles > INT32_MAX) return TQ_ERR_UNSUPPORTED;   // tile numbers are 32 bits wide
     constexpr int64_t kAround = 8;
     int64_t best = INT64_MAX;
     for (int s = 1; s <= kP4MaxSplit && s <= tiles; s *= 2) {

@@ -346,3 +346,38 @@ def test_prompt_chunk_value_sizes(tq, d, power):
     torch.cuda.synchronize()
     assert tq.device_status() == 0
     expect(out, ks, vs, q, hkv, np.arange(n)[None] <= (n - nq + np.arange(nq))[:, None], False, d == 256)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_captured_prompt_chunks_and_a_missing_page(tq, d):
+    """Two prompt chunks of different lengths captured into one graph and replayed with other queries;
+    then a page id outside the pool: reported, and what lies before it is not affected."""
+    r = rng(34, d)
+    hkv, hq, n, page = 4, 16, 700, 64
+    kc, vc, ks, vs = caches(tq, r, (n,), hkv, d, page)
+    spans = ((n - 130, 130), (100, 17))
+    qd = [torch.zeros(nq, hq, d, dtype=torch.float16, device=DEV) for _, nq in spans]
+    out = [torch.empty(nq, hq, d, device=DEV) for _, nq in spans]
+
+    def run():
+        for (pos0, _), a, b in zip(spans, qd, out):
+            tq.attn_prefill(kc, vc, a, b, pos0=pos0)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for turn in range(2):
+        q = [r.standard_normal((nq, hq, d)).astype(np.float16) for _, nq in spans]
+        for a, b in zip(qd, q):
+            a.copy_(dev(b))
+        if turn:
+            kc.page_table[0, 8] = 10 ** 7          # rows 512 .. 575
+        g.replay()
+        torch.cuda.synchronize()
+        assert tq.device_status() == (7 if turn else 0)
+        for (pos0, nq), a, b in list(zip(spans, q, out))[turn:]:
+            m = pos0 + nq
+            expect(b, ks[0][:m], vs[0][:m], a, hkv, np.arange(m)[None] <= (pos0 + np.arange(nq))[:, None], False, True)
+        assert torch.isfinite(out[0]).all()
